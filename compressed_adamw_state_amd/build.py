@@ -17,12 +17,13 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 # translation units of libflashopt.so: the fused step (hot path), the
 # uncompressed kinds, one tensor's codec and state, the codec ablations, the
-# measurement probes, the device schedules, the C ABI of tensor lists, and the
-# step that allocates nothing
+# measurement probes, the device schedules, the C ABI of tensor lists, the
+# step that allocates nothing, and the language-model operators (losses over
+# rows of logits; rows in 8 bits and the linear layer over them)
 UNITS = ["step.hip", "step_fp32.hip", "tensor.hip", "ablation.hip", "probe.hip", "schedule.hip",
-         "list.hip", "noalloc.hip"]
+         "list.hip", "noalloc.hip", "logits.hip", "int8.hip"]
 SOURCES = [os.path.join(CSRC, u) for u in UNITS] + [
-    os.path.join(CSRC, h) for h in ("codec.hpp", "device.hpp", "host.hpp", "quant.hpp")]
+    os.path.join(CSRC, h) for h in ("codec.hpp", "device.hpp", "host.hpp", "quant.hpp", "rows.hpp")]
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libflashopt.so")
 ARCH = os.environ.get("FLASHOPT_ARCH", "gfx950")

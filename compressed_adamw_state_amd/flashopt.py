@@ -1,4 +1,4 @@
-"""Thin Python binding of libflashopt.so (include/flashopt.h).
+"""Thin Python binding of libflashopt.so (include/flashopt.h, flashopt_lm.h).
 
 Argument marshalling only: each function below forwards to the C entry point
 of the same name; every step of the optimizer runs in the HIP kernels.  torch
@@ -87,6 +87,7 @@ class LionSchedule(ctypes.Structure):
 
 
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_D = ctypes.c_double
 SIGNATURES = {
     "flashopt_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "flashopt_split": (ctypes.c_int, [_P, _I64, _P, _P, _P]),
@@ -140,6 +141,30 @@ SIGNATURES = {
                                                ctypes.POINTER(SGDHparams), _I64, _P]),
     "flashopt_lion_step_range": (ctypes.c_int, [_P, _I32, _I32, ctypes.POINTER(_P),
                                                 ctypes.POINTER(LionHparams), _I64, _P]),
+    # include/flashopt_lm.h
+    "flashopt_logprob_workspace_bytes": (_SZ, [_I32, _I64, _I64, _I32]),
+    "flashopt_logprob": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _D, _P, _I32, _P, _SZ, _P, _P,
+                                        _P, _P, _P, _P]),
+    "flashopt_logprob_backward": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _D, _P, _P, _P, _P,
+                                                 _P, _I64, _P]),
+    "flashopt_logprob_grad": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _D, _P, _P, _P, _P, _SZ,
+                                             _P, _P, _P, _P, _I64, _P]),
+    "flashopt_distill_workspace_bytes": (_SZ, [_I32, _I64, _I64]),
+    "flashopt_distill": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _D, _P, _P, _I32, _I32, _P,
+                                        _SZ, _P, _P, _P]),
+    "flashopt_distill_backward": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _D, _P, _P, _I32, _P,
+                                                 _P, _P, _I64, _P]),
+    "flashopt_distill_grad": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _D, _P, _P, _I32, _I32,
+                                             _P, _P, _SZ, _P, _P, _P, _I64, _P]),
+    "flashopt_int8_ld": (_I64, [_I64]),
+    "flashopt_quantize_rows": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _P, _P, _P]),
+    "flashopt_tensor_quantize_rows": (ctypes.c_int, [ctypes.POINTER(Tensor), _I32, _I64, _P, _P,
+                                                     _P]),
+    "flashopt_int8_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "flashopt_int8_matmul": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _I32, _I64,
+                                            _P, _SZ, _P]),
+    "flashopt_int8_linear": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _I64,
+                                            _P, _SZ, _P]),
 }
 
 _lib = None
@@ -709,3 +734,219 @@ def build_list(theta_fp32: List[torch.Tensor], optimizer: str,
         states.append(st)
     lst = FlashoptList(states, grads, stream, optimizer)
     return states, lst
+
+
+# ---- language-model operators (include/flashopt_lm.h) -------------------------
+#
+# Tensors may live on any GPU: the call runs on theirs, on the given stream or
+# that device's current one.  `workspace`: a uint8 tensor of at least the
+# matching *_workspace_bytes, or None for one from torch's allocator.
+
+TYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+TOP_MAX = 64
+
+
+def element_type(t: torch.Tensor) -> int:
+    code = TYPE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"expected BF16, FP16 or FP32, not {t.dtype}")
+    return code
+
+
+def row_stride(t: torch.Tensor) -> int:
+    """Row stride of a 2-D tensor whose rows are dense."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("expected a 2-D tensor with dense rows")
+    if t.shape[0] <= 1:
+        return t.shape[1]
+    if t.stride(0) < t.shape[1]:
+        raise ValueError("rows overlap: make the tensor contiguous first")
+    return t.stride(0)
+
+
+def _arg(t: Optional[torch.Tensor], dtype, numel: int, device, name: str):
+    """Address of a dense device array of exactly numel elements, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != numel or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements on {device}")
+    return t.data_ptr()
+
+
+def _scratch(workspace, need: int, device):
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.dtype != torch.uint8 or workspace.device != device or \
+            not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    return workspace
+
+
+def _call(fn: str, device, stream, *args) -> None:
+    """The C call with `device` current, on the stream given or the device's own."""
+    if device.type != "cuda":
+        raise ValueError("expected device tensors")
+    current = torch.cuda.current_device()
+    if device.index == current:
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        status = getattr(lib(), fn)(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            if stream is None:
+                stream = torch.cuda.current_stream()
+            status = getattr(lib(), fn)(*args, stream.cuda_stream)
+    if status != 0:
+        raise FlashoptError(fn, status)
+
+
+def _logits(logits: torch.Tensor):
+    """(address, type, rows, vocab, stride) of 2-D logits."""
+    stride = row_stride(logits)
+    return logits.data_ptr(), element_type(logits), logits.shape[0], logits.shape[1], stride
+
+
+def _gradient(grad: torch.Tensor, logits: torch.Tensor):
+    if grad.dtype != logits.dtype or grad.shape != logits.shape or grad.device != logits.device:
+        raise ValueError("grad must have the logits' shape, type and device")
+    stride = row_stride(grad)
+    if grad.data_ptr() == logits.data_ptr() and stride != row_stride(logits):
+        raise ValueError("a gradient in the logits' place needs their stride")
+    return grad.data_ptr(), stride
+
+
+def flashopt_logprob(logits, targets=None, top: int = 0, temperature: float = 1.0, logprob=None,
+                     entropy=None, stats=None, top_logprob=None, top_id=None, workspace=None,
+                     stream=None) -> None:
+    """Outputs given as tensors (None: not computed): logprob, entropy [rows]
+    FP32, stats [rows, 4] FP32, top_logprob [rows, top] FP32, top_id [rows,
+    top] int64."""
+    x, ty, rows, vocab, stride = _logits(logits)
+    dev = logits.device
+    ws = _scratch(workspace, lib().flashopt_logprob_workspace_bytes(ty, rows, vocab, top), dev)
+    _call("flashopt_logprob", dev, stream, x, ty, rows, vocab, stride, temperature,
+          _arg(targets, torch.int64, rows, dev, "targets"), top, ws.data_ptr(), ws.numel(),
+          _arg(logprob, torch.float32, rows, dev, "logprob"),
+          _arg(entropy, torch.float32, rows, dev, "entropy"),
+          _arg(stats, torch.float32, 4 * rows, dev, "stats"),
+          _arg(top_logprob, torch.float32, rows * top, dev, "top_logprob"),
+          _arg(top_id, torch.int64, rows * top, dev, "top_id"))
+
+
+def flashopt_logprob_backward(logits, targets, stats, grad_logprob, grad_entropy, grad,
+                              temperature: float = 1.0, stream=None) -> None:
+    x, ty, rows, vocab, stride = _logits(logits)
+    dev = logits.device
+    g, gs = _gradient(grad, logits)
+    _call("flashopt_logprob_backward", dev, stream, x, ty, rows, vocab, stride, temperature,
+          _arg(targets, torch.int64, rows, dev, "targets"),
+          _arg(stats, torch.float32, 4 * rows, dev, "stats"),
+          _arg(grad_logprob, torch.float32, rows, dev, "grad_logprob"),
+          _arg(grad_entropy, torch.float32, rows, dev, "grad_entropy"), g, gs)
+
+
+def flashopt_logprob_grad(logits, targets, grad_logprob, grad_entropy, stats, grad, logprob=None,
+                          entropy=None, temperature: float = 1.0, workspace=None,
+                          stream=None) -> None:
+    x, ty, rows, vocab, stride = _logits(logits)
+    dev = logits.device
+    g, gs = _gradient(grad, logits)
+    ws = _scratch(workspace, lib().flashopt_logprob_workspace_bytes(ty, rows, vocab, 0), dev)
+    _call("flashopt_logprob_grad", dev, stream, x, ty, rows, vocab, stride, temperature,
+          _arg(targets, torch.int64, rows, dev, "targets"),
+          _arg(grad_logprob, torch.float32, rows, dev, "grad_logprob"),
+          _arg(grad_entropy, torch.float32, rows, dev, "grad_entropy"), ws.data_ptr(), ws.numel(),
+          _arg(logprob, torch.float32, rows, dev, "logprob"),
+          _arg(entropy, torch.float32, rows, dev, "entropy"),
+          _arg(stats, torch.float32, 4 * rows, dev, "stats"), g, gs)
+
+
+def _listed(top_id, top_logprob, rows: int, dev):
+    if top_id.dim() != 2 or top_id.shape != top_logprob.shape:
+        raise ValueError("top_id and top_logprob must both be rows x top")
+    top = top_id.shape[1]
+    return (_arg(top_id, torch.int64, rows * top, dev, "top_id"),
+            _arg(top_logprob, torch.float32, rows * top, dev, "top_logprob"), top)
+
+
+def flashopt_distill(logits, top_id, top_logprob, loss, stats, tail: bool = True,
+                     temperature: float = 1.0, workspace=None, stream=None) -> None:
+    x, ty, rows, vocab, stride = _logits(logits)
+    dev = logits.device
+    ids, tlp, top = _listed(top_id, top_logprob, rows, dev)
+    ws = _scratch(workspace, lib().flashopt_distill_workspace_bytes(ty, rows, vocab), dev)
+    _call("flashopt_distill", dev, stream, x, ty, rows, vocab, stride, temperature, ids, tlp, top,
+          int(tail), ws.data_ptr(), ws.numel(), _arg(loss, torch.float32, rows, dev, "loss"),
+          _arg(stats, torch.float32, 8 * rows, dev, "stats"))
+
+
+def flashopt_distill_backward(logits, top_id, top_logprob, stats, grad_loss, grad,
+                              temperature: float = 1.0, stream=None) -> None:
+    x, ty, rows, vocab, stride = _logits(logits)
+    dev = logits.device
+    ids, tlp, top = _listed(top_id, top_logprob, rows, dev)
+    g, gs = _gradient(grad, logits)
+    _call("flashopt_distill_backward", dev, stream, x, ty, rows, vocab, stride, temperature, ids,
+          tlp, top, _arg(stats, torch.float32, 8 * rows, dev, "stats"),
+          _arg(grad_loss, torch.float32, rows, dev, "grad_loss"), g, gs)
+
+
+def flashopt_distill_grad(logits, top_id, top_logprob, grad_loss, loss, stats, grad,
+                          tail: bool = True, temperature: float = 1.0, workspace=None,
+                          stream=None) -> None:
+    x, ty, rows, vocab, stride = _logits(logits)
+    dev = logits.device
+    ids, tlp, top = _listed(top_id, top_logprob, rows, dev)
+    g, gs = _gradient(grad, logits)
+    ws = _scratch(workspace, lib().flashopt_distill_workspace_bytes(ty, rows, vocab), dev)
+    _call("flashopt_distill_grad", dev, stream, x, ty, rows, vocab, stride, temperature, ids, tlp,
+          top, int(tail), _arg(grad_loss, torch.float32, rows, dev, "grad_loss"), ws.data_ptr(),
+          ws.numel(), _arg(loss, torch.float32, rows, dev, "loss"),
+          _arg(stats, torch.float32, 8 * rows, dev, "stats"), g, gs)
+
+
+def flashopt_quantize_rows(x, codes, scale, stream=None) -> None:
+    """x [rows, cols] -> codes [rows, flashopt_int8_ld(cols)] int8, scale [rows] FP32."""
+    rows, cols = x.shape
+    ld = lib().flashopt_int8_ld(cols)
+    _call("flashopt_quantize_rows", x.device, stream, x.data_ptr(), element_type(x), rows, cols,
+          row_stride(x), _arg(codes, torch.int8, rows * ld, x.device, "codes"),
+          _arg(scale, torch.float32, rows, x.device, "scale"))
+
+
+def flashopt_tensor_quantize_rows(st: TensorState, cols: int, codes, scale, stream=None) -> None:
+    """The state's master weight as numel / cols rows in 8 bits."""
+    if cols < 1 or st.numel % cols:
+        raise ValueError(f"{st.numel} elements are not rows of {cols}")
+    rows, ld, dev = st.numel // cols, lib().flashopt_int8_ld(cols), st.theta.device
+    d = st.descriptor()
+    _call("flashopt_tensor_quantize_rows", dev, stream, ctypes.byref(d), st.kind, cols,
+          _arg(codes, torch.int8, rows * ld, dev, "codes"),
+          _arg(scale, torch.float32, rows, dev, "scale"))
+
+
+def flashopt_int8_matmul(a, a_scale, b, b_scale, k: int, out, bias=None, workspace=None,
+                         stream=None) -> None:
+    """out [m, n] from codes a [m, ld], b [n, ld] with ld = flashopt_int8_ld(k)."""
+    m, n = out.shape
+    dev = out.device
+    ld = lib().flashopt_int8_ld(k)
+    ws = _scratch(workspace, lib().flashopt_int8_workspace_bytes(m, n, k), dev)
+    _call("flashopt_int8_matmul", dev, stream, _arg(a, torch.int8, m * ld, dev, "a"),
+          _arg(a_scale, torch.float32, m, dev, "a_scale"), _arg(b, torch.int8, n * ld, dev, "b"),
+          _arg(b_scale, torch.float32, n, dev, "b_scale"), _arg(bias, out.dtype, n, dev, "bias"),
+          m, n, k, out.data_ptr(), element_type(out), row_stride(out), ws.data_ptr(), ws.numel())
+
+
+def flashopt_int8_linear(x, w, w_scale, out, bias=None, workspace=None, stream=None) -> None:
+    """out [m, n] from x [m, k] of out's type and codes w [n, flashopt_int8_ld(k)]."""
+    (m, k), n = x.shape, out.shape[1]
+    dev = out.device
+    if out.shape[0] != m or out.dtype != x.dtype or x.device != dev:
+        raise ValueError("x and out must have the same rows, type and device")
+    ld = lib().flashopt_int8_ld(k)
+    ws = _scratch(workspace, lib().flashopt_int8_workspace_bytes(m, n, k), dev)
+    _call("flashopt_int8_linear", dev, stream, x.data_ptr(), element_type(x), m, k, row_stride(x),
+          _arg(w, torch.int8, n * ld, dev, "w"), _arg(w_scale, torch.float32, n, dev, "w_scale"),
+          _arg(bias, out.dtype, n, dev, "bias"), n, out.data_ptr(), row_stride(out),
+          ws.data_ptr(), ws.numel())

@@ -51,6 +51,7 @@ from typing import Iterable, List, Optional
 import torch
 
 from . import flashopt as F
+from .int8 import Int8Weight
 
 # Placement of the codes in a checkpoint's "codes" tensors (include/flashopt.h):
 # "blocks512" -- AdamW's rho, m and v planes per 512-element block, SGD's and
@@ -410,6 +411,16 @@ class _FlashOptimizer(torch.optim.Optimizer):
         v = torch.empty_like(th) if self.kind == "adamw" else None
         F.flashopt_tensor_export(st, th, m, v)
         return th, m, v
+
+    def export_int8(self, p: torch.Tensor) -> Int8Weight:
+        """One parameter's master weight in 8 bits with a scale for each
+        output channel (its first dimension), straight from the state: the
+        weight of an int8.Int8Linear, for evaluating or teaching from the
+        trained model."""
+        self._join_release()
+        if p.dim() < 2:
+            raise ValueError("export_int8 needs a matrix")
+        return Int8Weight.from_state(self.state[p]["flash"], p.numel() // p.shape[0])
 
 
 class FlashAdamW(_FlashOptimizer):

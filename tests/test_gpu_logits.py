@@ -1,0 +1,337 @@
+"""The losses over rows of logits (include/flashopt_lm.h, losses.py) against
+plain 64-bit forms (lm_plain.py, which derives the tolerances): log
+probabilities, entropy, top alternatives, distillation, and their gradients,
+over types, odd vocabularies around the kernels' chunk sizes, strided and
+misaligned rows, masks, ties, and rows whose mask leaves nothing."""
+import math
+
+import pytest
+import torch
+
+import lm_plain as P
+from compressed_adamw_state_amd import flashopt as F
+from compressed_adamw_state_amd import losses as L
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+VOCABS = [1, 2, 7, 8, 9, 64, 65, 1000, 4095, 8191, 8193, 16383, 16385, 50257, 131073]
+
+
+def near(got, ref, tol, dtype=torch.float32):
+    """got (of dtype) is within tol and half a step of ref; equal where ref is not finite."""
+    got, ref = got.double().cpu(), ref.cpu()
+    fin = torch.isfinite(ref)
+    assert torch.equal(got[~fin].nan_to_num(7e300), ref[~fin].nan_to_num(7e300))
+    tol = tol.cpu() if torch.is_tensor(tol) else torch.full_like(ref, tol)
+    lim = tol * (1 + P.half_step(dtype)) + P.half_step(dtype) * ref.abs() + P.smallest(dtype) + 2.0 ** -126
+    bad = fin & ~((got - ref).abs() <= lim)
+    if bool(bad.any()):
+        k = torch.where(fin, (got - ref).abs() / lim, 0.0).flatten().argmax()
+        raise AssertionError(f"{int(bad.sum())} of {ref.numel()} outside; worst at {int(k)}: "
+                             f"{got.flatten()[k].item()} for {ref.flatten()[k].item()}, "
+                             f"allowed {lim.flatten()[k].item()}")
+
+
+def draw(rows, vocab, dtype, seed, masked=False, scale=3.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, vocab, generator=g) * scale
+    if masked:
+        x[torch.rand(rows, vocab, generator=g) < 0.5] = -math.inf
+    t = torch.randint(0, vocab, (rows,), generator=g)
+    if rows > 2:
+        t[1] = -100
+        t[2] = vocab + 5
+    return x.to(dtype), t, g
+
+
+def place(x, how):
+    """The logits on the GPU: dense, or as rows of a wider buffer, or starting one element in."""
+    if how == "dense":
+        return x.cuda()
+    rows, vocab = x.shape
+    if how == "strided":
+        buf = torch.full((rows, vocab + 13), 1e4 if x.dtype != torch.float32 else 1e30, dtype=x.dtype, device="cuda")
+        v = buf[:, 3:3 + vocab]
+    else:
+        buf = torch.zeros(rows * vocab + 1, dtype=x.dtype, device="cuda")
+        v = buf[1:].view(rows, vocab)
+    v.copy_(x)
+    return v
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", VOCABS)
+def test_logprob_entropy_top(dtype, vocab):
+    for rows, how, masked, temp in ((1, "dense", False, 1.0), (5, "strided", True, 0.7), (3, "offset", False, 2.5)):
+        x, t, _ = draw(rows, vocab, dtype, vocab + rows, masked)
+        k = min(64, vocab) if rows == 1 else min(5, vocab)
+        r = L.token_logprobs(place(x, how), t.cuda(), top=k, temperature=temp)
+        lp, lt, en, et = P.logprob(x, t, temp)
+        near(r.logprob, lp, lt)
+        near(r.entropy, en, et)
+        ids = P.top(x, k)
+        assert torch.equal(r.top_id.cpu(), ids)
+        for c in range(k):
+            v, vt, _, _ = P.logprob(x, ids[:, c], temp)
+            near(r.top_logprob[:, c], v, vt)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_ties_go_to_the_lowest_id(dtype):
+    vocab = 40000
+    g = torch.Generator().manual_seed(5)
+    few = torch.randint(-2, 3, (4, vocab), generator=g).float() * 0.5     # five values, 8000 of each
+    few[1] = 0.25                                                         # one value
+    few[2] = -math.inf
+    few[2, 33333] = 1.0                                                   # one token allowed
+    few[3, ::2] = 0.0
+    few[3, 1::2] = -0.0                                                   # equal as numbers
+    x = few.to(dtype)
+    for k in (1, 20, 64):
+        r = L.token_logprobs(x.cuda(), top=k)
+        assert torch.equal(r.top_id.cpu(), P.top(x, k))
+    assert r.logprob is None
+    near(r.entropy, P.logprob(x, torch.zeros(4, dtype=torch.int64), 1.0)[2], 1e-4)
+    assert r.top_logprob[2, 0].item() == 0.0 and r.top_logprob[2, 1].item() == -math.inf
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_top_in_one_thread(dtype):
+    """The largest entries next to each other, and entries in falling and rising order."""
+    vocab = 30000
+    x = torch.randn(4, vocab, generator=torch.Generator().manual_seed(3))
+    x[0, 10000:10064] = torch.arange(64).float() + 10
+    x[1] = -torch.arange(vocab).float() / 64
+    x[2] = torch.arange(vocab).float() / 64
+    x = x.to(dtype)
+    for k in (3, 64):
+        assert torch.equal(L.token_logprobs(x.cuda(), top=k).top_id.cpu(), P.top(x, k))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_special_rows(dtype):
+    vocab, low = 9000, torch.finfo(dtype).min
+    x = torch.randn(8, vocab, generator=torch.Generator().manual_seed(8))
+    x[0] = -math.inf                                       # nothing left
+    x[1] = low                                             # the lowest value everywhere: uniform
+    x[2, 1:] = low                                         # masked by the lowest value
+    x[3] = torch.finfo(dtype).max / 2
+    x[3, 7] = torch.finfo(dtype).max
+    x[4, 100] = math.nan
+    x[5, 100] = math.inf
+    x[6, 1:] = -math.inf
+    x = x.to(dtype)
+    t = torch.tensor([3, 4, 0, 7, 5, 5, 0, 11])
+    xc = x.cuda().requires_grad_()
+    r = L.token_logprobs(xc, t.cuda(), top=4)
+    lp, lt, en, et = P.logprob(x, t, 1.0)
+    ok = [0, 1, 2, 3, 6, 7]
+    near(r.logprob[ok].detach(), lp[ok], lt[ok])
+    near(r.entropy[ok].detach(), en[ok], et[ok])
+    assert lp[0].item() == -math.inf and abs(en[1].item() - math.log(vocab)) < 1e-9
+    assert bool(torch.isnan(r.logprob[[4, 5]]).all()) and bool(torch.isnan(r.entropy[[4, 5]]).all())
+    assert torch.equal(r.top_id[ok].cpu(), P.top(x, 4)[ok])
+    assert bool(((r.top_id >= 0) & (r.top_id < vocab)).all())
+    gl, gh = torch.arange(1.0, 9.0), torch.linspace(-1, 1, 8)
+    gr, = torch.autograd.grad((r.logprob, r.entropy), xc, (gl.cuda(), gh.cuda()))
+    ref, tol = P.logprob_grad(x[ok], t[ok], gl[ok], gh[ok], 1.0)
+    near(gr[ok], ref, tol, dtype)
+    assert bool((gr[0] == 0).all())
+    ids = torch.tensor([[0, 5, 7, 7, -1]] * 8)
+    tlp = torch.log(torch.tensor([[0.3, 0.2, 0.1, 0.1, 0.25]] * 8))
+    for tail in (False, True):
+        loss, gd = L.distill_grad(xc.detach(), ids.cuda(), tlp.cuda(), gl.cuda(), tail=tail)
+        fin = [0, 1, 3, 7]                                 # the rest have infinite loss or NaN
+        a, at, b, bt = P.distill(x[fin], ids[fin], tlp[fin], tail, 1.0, gl[fin])
+        near(loss[fin], a, at)
+        near(gd[fin], b, bt, dtype)
+        assert loss[0].item() == 0 and bool((gd[0] == 0).all())
+        assert loss[6].item() == math.inf
+        assert bool(torch.isnan(loss[[4, 5]]).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", VOCABS)
+def test_logprob_gradient(dtype, vocab):
+    for rows, how, masked, temp in ((1, "dense", False, 1.0), (5, "strided", True, 0.7), (3, "offset", False, 2.5)):
+        x, t, g = draw(rows, vocab, dtype, 3 * vocab + rows, masked)
+        gl, gh = torch.randn(rows, generator=g), torch.randn(rows, generator=g)
+        xg = place(x, how).requires_grad_()
+        r = L.token_logprobs(xg, t.cuda(), temperature=temp)
+        for a, b in ((gl, gh), (gl, None), (None, gh)):
+            outs = [o for o, u in ((r.logprob, a), (r.entropy, b)) if u is not None]
+            ups = [u.cuda() for u in (a, b) if u is not None]
+            got, = torch.autograd.grad(outs, xg, ups, retain_graph=True)
+            ref, tol = P.logprob_grad(x, t, a, b, temp)
+            near(got, ref, tol, dtype)
+        one = L.token_logprobs_grad(place(x, how), t.cuda(), gl.cuda(), gh.cuda(), temperature=temp)
+        ref, tol = P.logprob_grad(x, t, gl, gh, temp)
+        near(one.grad, ref, tol, dtype)
+        lp, lt, en, et = P.logprob(x, t, temp)
+        near(one.logprob, lp, lt)
+        near(one.entropy, en, et)
+        dense = place(x, how)                              # the gradient in the logits' place
+        around = dense._base.clone() if how == "strided" else None
+        two = L.token_logprobs_grad(dense, t.cuda(), gl.cuda(), None, temperature=temp, inplace=True)
+        assert two.grad.data_ptr() == dense.data_ptr()
+        ref, tol = P.logprob_grad(x, t, gl, None, temp)
+        near(dense, ref, tol, dtype)
+        if how == "strided":                               # what lies between the rows stays
+            assert torch.equal(around[:, :3], dense._base[:, :3])
+            assert torch.equal(around[:, 3 + vocab:], dense._base[:, 3 + vocab:])
+
+
+def teacher(x, k, temp, seed):
+    g = torch.Generator().manual_seed(seed)
+    z = (x.double() + torch.randn(x.shape, generator=g)) / temp
+    v, i = torch.topk(z, k, dim=1)
+    return i, (v - torch.logsumexp(z, 1, keepdim=True)).float()
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", VOCABS)
+def test_distill(dtype, vocab, tail):
+    for rows, how, temp, k in ((1, "dense", 1.0, 64), (4, "strided", 0.7, 1), (3, "offset", 2.0, 17)):
+        k = min(k, vocab)
+        x, _, g = draw(rows, vocab, dtype, 7 * vocab + rows)
+        ids, tlp = teacher(x, k, temp, vocab)
+        up = torch.randn(rows, generator=g)
+        a, at, b, bt = P.distill(x, ids, tlp, tail, temp, up)
+        loss, grad = L.distill_grad(place(x, how), ids.cuda(), tlp.cuda(), up.cuda(), tail=tail, temperature=temp)
+        near(loss, a, at)
+        near(grad, b, bt, dtype)
+        xg = place(x, how).requires_grad_()
+        lo = L.distill_loss(xg, ids.cuda(), tlp.cuda(), tail=tail, temperature=temp)
+        near(lo.detach(), a, at)
+        got, = torch.autograd.grad(lo, xg, up.cuda())
+        near(got, b, bt, dtype)
+        here = place(x, how)
+        L.distill_grad(here, ids.cuda(), tlp.cuda(), up.cuda(), tail=tail, temperature=temp, inplace=True)
+        near(here, b, bt, dtype)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_distill_odd_lists(dtype, tail):
+    """Repeated ids, skipped ids, none at all, all of the vocabulary, a student far from the teacher."""
+    vocab, rows = 20000, 6
+    x, _, g = draw(rows, vocab, dtype, 77, scale=2.0)
+    ids, tlp = teacher(x, 8, 1.0, 5)
+    ids[0, 3] = ids[0, 1]
+    ids[0, 7] = ids[0, 1]
+    ids[1, 0], ids[1, 5] = -100, vocab
+    ids[2, :] = -1
+    x[3] -= 0.0
+    x[3, ids[3]] = -30.0                                   # the student finds them unlikely
+    x[4] = -30.0
+    x[4, ids[4]] = 30.0                                    # the student finds nothing else likely
+    tlp[5] = -math.inf
+    tlp[5, 2] = 0.0                                        # the teacher knows one token
+    up = torch.randn(rows, generator=g)
+    a, at, b, bt = P.distill(x, ids, tlp, tail, 1.0, up)
+    loss, grad = L.distill_grad(x.cuda(), ids.cuda(), tlp.cuda(), up.cuda(), tail=tail)
+    near(loss, a, at)
+    near(grad, b, bt, dtype)
+    assert loss[2].item() == 0 and bool((grad[2] == 0).all())
+    whole = torch.arange(50).repeat(2, 1)
+    y = torch.randn(2, 50, generator=g).to(dtype)
+    t = torch.log_softmax(torch.randn(2, 50, generator=g).double(), 1).float()
+    a, at, b, bt = P.distill(y, whole, t, tail, 1.0, up[:2])
+    loss, grad = L.distill_grad(y.cuda(), whole.cuda(), t.cuda(), up[:2].cuda(), tail=tail)
+    near(loss, a, at)
+    near(grad, b, bt, dtype)
+
+
+def test_gradients_against_differences():
+    """Central differences of the library's own losses in FP32, h = 2^-5: the
+    third derivatives of these losses are below 2 (weights at most 1), so the
+    difference is off by h^2 / 3 < 4e-4, and the losses' own rounding of at
+    most 2e-5 adds 2e-5 / h = 7e-4."""
+    vocab, h = 37, 2.0 ** -5
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(1, vocab, generator=g)
+    both = torch.cat([x + h * torch.eye(vocab), x - h * torch.eye(vocab)]).cuda()
+    t = torch.full((2 * vocab,), 5)
+    r = L.token_logprobs(both, t.cuda())
+    f = 0.5 * r.logprob + 0.25 * r.entropy
+    diff = (f[:vocab] - f[vocab:]) / (2 * h)
+    one = L.token_logprobs_grad(x.cuda(), t[:1].cuda(), torch.tensor([0.5]).cuda(), torch.tensor([0.25]).cuda())
+    assert (diff - one.grad[0]).abs().max().item() < 1.1e-3
+    ids, tlp = teacher(x, 6, 1.0, 2)
+    for tail in (False, True):
+        f = L.distill_loss(both, ids.repeat(2 * vocab, 1).cuda(), tlp.repeat(2 * vocab, 1).cuda(), tail=tail)
+        diff = (f[:vocab] - f[vocab:]) / (2 * h)
+        _, grad = L.distill_grad(x.cuda(), ids.cuda(), tlp.cuda(), torch.ones(1).cuda(), tail=tail)
+        assert (diff - grad[0]).abs().max().item() < 1.1e-3
+
+
+def test_many_rows_and_shapes():
+    """More rows than the GPU holds blocks at once; leading dimensions; no rows."""
+    x, t, g = draw(3000, 1003, torch.bfloat16, 9)
+    r = L.token_logprobs(x.cuda().view(30, 100, 1003), t.cuda().view(30, 100), top=3)
+    lp, lt, en, et = P.logprob(x, t, 1.0)
+    assert r.logprob.shape == (30, 100) and r.top_id.shape == (30, 100, 3)
+    near(r.logprob.view(-1), lp, lt)
+    near(r.entropy.view(-1), en, et)
+    assert torch.equal(r.top_id.view(-1, 3).cpu(), P.top(x, 3))
+    up = torch.rand(3000, generator=g)
+    ids, tlp = teacher(x, 5, 1.0, 4)
+    a, at, b, bt = P.distill(x, ids, tlp, True, 1.0, up)
+    loss, grad = L.distill_grad(x.cuda(), ids.cuda(), tlp.cuda(), up.cuda())
+    near(loss, a, at)
+    near(grad, b, bt, torch.bfloat16)
+    none = L.token_logprobs(torch.empty(0, 10, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda"), top=2)
+    assert none.logprob.shape == (0,) and none.top_id.shape == (0, 2)
+    vec = L.token_logprobs(x[7].cuda(), t[7].cuda(), top=1)
+    near(vec.logprob.view(1), lp[7:8], lt[7:8])
+
+
+def test_other_stream_and_repeat():
+    """The same call twice gives the same bits, on the default and on a side stream."""
+    x, t, g = draw(65, 50257, torch.float16, 21)
+    xc, tc = x.cuda(), t.cuda()
+    up = torch.randn(65, generator=g).cuda()
+    ids, tlp = (v.cuda() for v in teacher(x, 20, 1.0, 3))
+
+    def both():
+        r = L.token_logprobs(xc, tc, top=7)
+        return (r.logprob, r.entropy, r.top_logprob, r.top_id, *L.distill_grad(xc, ids, tlp, up),
+                L.token_logprobs_grad(xc, tc, up, up).grad)
+    first = both()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        second = both()
+    torch.cuda.synchronize()
+    for a, b in zip(first, second):
+        assert torch.equal(a, b)
+
+
+def test_captured_and_replayed():
+    """The one-call forms in a HIP graph, replayed over new logits with eager work in between."""
+    rows, vocab = 9, 33001
+    x, t, _ = draw(rows, vocab, torch.bfloat16, 31)
+    ids, tlp = teacher(x, 12, 1.0, 1)
+    xs, ts, ids, tlp = x.cuda(), t.cuda(), ids.cuda(), tlp.cuda()
+    up = torch.linspace(-1, 1, rows, device="cuda")
+
+    def work():
+        r = L.token_logprobs(xs, ts, top=9)
+        return (r.logprob, r.top_id, *L.distill_grad(xs, ids, tlp, up), L.token_logprobs_grad(xs, ts, up).grad)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = work()
+    for k in range(3):
+        xs.copy_(draw(rows, vocab, torch.bfloat16, 50 + k)[0])
+        eager = [o.clone() for o in work()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(held, eager):
+            assert torch.equal(a, b)
