@@ -13,6 +13,7 @@
 namespace flashopt {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int64_t kLdStep = 128;
 static inline int64_t ld_of(int64_t cols) { return (cols + kLdStep - 1) / kLdStep * kLdStep; }
@@ -92,40 +93,283 @@ __global__ __launch_bounds__(kBlock) void quantize_state_kernel(DevTensor d, int
     quantize_row(load, cols, ld, codes + row * ld, scale + row);
 }
 
-// ---- the product ----------------------------------------------------------------
+// ---- the product: tiles -----------------------------------------------------------
 
-// One wave per 16 x 16 outputs: v_mfma_i32_16x16x64_i8 with the weight rows as
-// its A rows and the tokens as its B columns; lane l holds 16 consecutive
-// codes of row l % 16, at (l / 16) * 16, and afterwards the four outputs
-// 4 (l / 16) .. + 3 of token l % 16.
-template <int kType>
-__global__ __launch_bounds__(kBlock) void matmul_kernel(const int8_t* a, const float* a_scale,
-                                                        const int8_t* b, const float* b_scale,
-                                                        const typename Elem<kType>::T* bias,
-                                                        int64_t m, int64_t n, int64_t ld,
-                                                        typename Elem<kType>::T* out,
-                                                        int64_t out_stride) {
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int64_t n0 = ((int64_t)blockIdx.x * kWavesPerBlock + wave) * 16;
-    const int64_t m0 = (int64_t)blockIdx.y * 16;
-    if (n0 >= n) return;
-    const int64_t wr = min(n0 + (lane & 15), n - 1), xr = min(m0 + (lane & 15), m - 1);
-    const int8_t* w = b + wr * ld + (lane >> 4) * 16;
-    const int8_t* x = a + xr * ld + (lane >> 4) * 16;
-    i32x4 acc = {0, 0, 0, 0};
-    for (int64_t k = 0; k < ld; k += 64)
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(*(const i32x4*)(w + k), *(const i32x4*)(x + k),
-                                                    acc, 0, 0, 0);
-    const int64_t i = m0 + (lane & 15);
-    if (i >= m) return;
-    const float s = a_scale[i];
+// A block computes BN output channels x BM tokens with WN x WM waves, each FN x
+// FM products of v_mfma_i32_32x32x32_i8 (the weight rows as A, the tokens as
+// B: lane l holds 16 codes of row l % 32; afterwards, of token l % 32, the
+// channels 8 (r / 4) + 4 (l / 32) + r % 4).  Stages of 128 codes (one line of
+// each row) go global -> registers -> LDS, two in LDS, in four steps of 32 codes:
+//   step 0, 1: half of the next stage's registers each go to its LDS half,
+//   step 1, 2: and the loads of the stage after it are issued into them;
+//   barrier:   the next stage is written, this one read;
+//   step 3:    the next stage's first fragments are read.
+// Each step reads the next step's fragments, and its products are spread over
+// what it issues (sched_group_barrier).  A row of 128 bytes keeps its word c
+// at c ^ (row & 7), so that the 8 rows read or the 8 words written at a time
+// lie in different banks.
+constexpr int kStage = 128;
+
+template <int kType, int FN, int FM, int WN, int WM>
+struct Tile {
+    static constexpr int kThreads = WN * WM * kWave;
+    static constexpr int BN = WN * FN * 32, BM = WM * FM * 32;
+    static constexpr int kStageBytes = (BN + BM) * kStage;
+    static constexpr int kLoads = kStageBytes / 16 / kThreads;
+    static constexpr int kRowsPerLoad = kThreads / 8;
+    static constexpr int kOutPad = 16;           // bytes behind each row of the output strip
+    static constexpr size_t kLds = 2 * kStageBytes;
+};
+
+// Which tile a block takes.  Blocks go to the 8 XCDs by turns; each XCD gets a
+// run of tiles of its own, ordered in columns of at most 8 token tiles, so that
+// the tiles an XCD works on at a time share rows in its L2.
+__device__ __forceinline__ void tile_of(uint32_t block, uint32_t tn, uint32_t tm, uint32_t& n,
+                                        uint32_t& m) {
+    const uint32_t total = tn * tm, xcd = block % 8, k = block / 8;
+    const uint32_t q = total / 8, r = total % 8;
+    const uint32_t t = xcd * q + (xcd < r ? xcd : r) + k;
+    const uint32_t group = 8 * tn, g = t / group, in = t % group;
+    const uint32_t high = tm - g * 8 < 8 ? tm - g * 8 : 8;
+    m = g * 8 + in % high;
+    n = in / high;
+}
+
+template <int kType, int FN, int FM, int WN, int WM>
+__global__ __launch_bounds__(WN * WM * kWave, 1) void tile_kernel(
+    const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
+    const typename Elem<kType>::T* bias, int64_t m, int64_t n, int32_t ld, uint32_t tn, uint32_t tm,
+    typename Elem<kType>::T* out, int64_t out_stride) {
+    typedef Tile<kType, FN, FM, WN, WM> S;
+    typedef typename Elem<kType>::T T;
+    extern __shared__ __attribute__((aligned(16))) int8_t lds[];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const int wn = wave % WN, wm = wave / WN;
+    uint32_t in_, im_;
+    tile_of(blockIdx.x, tn, tm, in_, im_);
+    const int64_t n0 = (int64_t)in_ * S::BN, m0 = (int64_t)im_ * S::BM;
+    const int8_t* wbase = b + n0 * ld;
+    const int8_t* xbase = a + m0 * ld;
+    const int nlast = (int)(n - n0 < S::BN ? n - n0 : S::BN) - 1;
+    const int mlast = (int)(m - m0 < S::BM ? m - m0 : S::BM) - 1;
+
+    // this thread's words of a stage: row r0 + i * kRowsPerLoad, word tid % 8
+    const int r0 = tid / 8, c0 = tid % 8;
+    uint32_t off[S::kLoads];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int64_t j = n0 + (lane >> 4) * 4 + r;
-        if (j >= n) continue;
-        float y = (float)acc[r] * (s * b_scale[j]);
-        if (bias) y += Elem<kType>::up(bias[j]);
-        out[i * out_stride + j] = Elem<kType>::down(y);
+    for (int i = 0; i < S::kLoads; ++i) {
+        const int r = r0 + i * S::kRowsPerLoad;
+        // rows past the end read the last row; their products are not stored
+        const int g = r < S::BN ? min(r, nlast) : min(r - S::BN, mlast);
+        off[i] = (uint32_t)g * (uint32_t)ld + c0 * 16;
+    }
+    const int wslot = r0 * kStage + ((c0 ^ (r0 & 7)) * 16);
+    i32x4 g[S::kLoads];
+    constexpr int kHalf = S::kLoads / 2;
+    auto fetch = [&](int s, int from, int to) {
+#pragma unroll
+        for (int i = 0; i < S::kLoads; ++i) {
+            if (i < from || i >= to) continue;
+            const int8_t* p = (i * S::kRowsPerLoad < S::BN ? wbase : xbase) + (int64_t)s * kStage;
+            g[i] = *(const i32x4*)(p + off[i]);
+        }
+    };
+    auto put = [&](int s, int from, int to) {
+        int8_t* d = lds + (s & 1) * S::kStageBytes + wslot;
+#pragma unroll
+        for (int i = 0; i < S::kLoads; ++i)
+            if (i >= from && i < to) *(i32x4*)(d + i * S::kRowsPerLoad * kStage) = g[i];
+    };
+    i32x4 fa[2][FN], fb[2][FM];
+    const int ra = (wn * FN * 32 + (lane & 31)) * kStage;
+    const int rb = (S::BN + wm * FM * 32 + (lane & 31)) * kStage;
+    int slot[4];
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) slot[ks] = ((ks * 2 + (lane >> 5)) ^ (lane & 7)) * 16;
+    auto read = [&](int p, int s, int ks) {
+        const int8_t* d = lds + (s & 1) * S::kStageBytes + slot[ks];
+#pragma unroll
+        for (int f = 0; f < FN; ++f) fa[p][f] = *(const i32x4*)(d + ra + f * 32 * kStage);
+#pragma unroll
+        for (int f = 0; f < FM; ++f) fb[p][f] = *(const i32x4*)(d + rb + f * 32 * kStage);
+    };
+    i32x16 acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+    auto products = [&](int p) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[p][i], fb[p][j], acc[i][j], 0, 0, 0);
+    };
+    // a step's order: its products with the LDS reads, then the writes, then the
+    // loads between them
+    constexpr int kReads = FN + FM, kProducts = FN * FM;
+#define TILE_STEP(writes, loads)                                                     \
+    do {                                                                             \
+        constexpr int kFirst = kProducts / 4;                                        \
+        _Pragma("unroll") for (int q = 0; q < kFirst; ++q) {                         \
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                       \
+            __builtin_amdgcn_sched_group_barrier(0x100, kReads / kFirst, 0);         \
+        }                                                                            \
+        _Pragma("unroll") for (int q = 0; q < kProducts - kFirst; ++q) {             \
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                       \
+            if ((writes) && q < kHalf) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0); \
+            if ((loads) && q < kHalf) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0); \
+        }                                                                            \
+        __builtin_amdgcn_sched_barrier(0);                                           \
+    } while (0)
+    const int stages = ld / kStage;
+    fetch(0, 0, S::kLoads);
+    put(0, 0, S::kLoads);
+    fetch(stages > 1 ? 1 : 0, 0, S::kLoads);
+    __syncthreads();
+    read(0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    for (int s = 0; s + 1 < stages; ++s) {
+        const int ahead = s + 2 < stages ? s + 2 : s + 1;        // the last: loaded, not used
+        read(1, s, 1);
+        products(0);
+        put(s + 1, 0, kHalf);
+        TILE_STEP(true, false);
+        read(0, s, 2);
+        products(1);
+        put(s + 1, kHalf, S::kLoads);
+        fetch(ahead, 0, kHalf);
+        TILE_STEP(true, true);
+        read(1, s, 3);
+        products(0);
+        fetch(ahead, kHalf, S::kLoads);
+        TILE_STEP(false, true);
+        __syncthreads();
+        read(0, s + 1, 0);
+        products(1);
+        TILE_STEP(false, false);
+    }
+#undef TILE_STEP
+    read(1, stages - 1, 1);
+    products(0);
+    read(0, stages - 1, 2);
+    products(1);
+    read(1, stages - 1, 3);
+    products(0);
+    products(1);
+    __syncthreads();                             // the strips below replace the stages
+
+    // Out through LDS, a strip of 32 tokens x FN * 32 channels of a wave at a
+    // time, so that rows are stored in 16-byte words one after another.
+    constexpr int kRowBytes = FN * 32 * (int)sizeof(T) + S::kOutPad;
+    static_assert(32 * kRowBytes * WN * WM <= (int)S::kLds, "strips fit");
+    int8_t* strip = lds + wave * (32 * kRowBytes);
+    const int64_t nw = n0 + wn * FN * 32;
+    float ws[FN][16], bs[FN][16];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int64_t j = nw + i * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
+            ws[i][r] = j < n ? b_scale[j] : 0.0f;
+            bs[i][r] = bias && j < n ? Elem<kType>::up(bias[j]) : 0.0f;
+        }
+    constexpr int kWords = FN * 32 * (int)sizeof(T) / 16;          // 16-byte words of a strip's row
+    constexpr int E = Elem<kType>::kE;
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+        const int64_t mf = m0 + (wm * FM + f) * 32;
+        const float s = mf + (lane & 31) < m ? a_scale[mf + (lane & 31)] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y[e] = (float)acc[i][f][r + e] * (s * ws[i][r + e]);
+                    if (bias) y[e] += bs[i][r + e];
+                }
+                int8_t* d = strip + (lane & 31) * kRowBytes +
+                            (i * 32 + 8 * (r / 4) + 4 * (lane >> 5)) * (int)sizeof(T);
+                if (kType == FLASHOPT_FP32) {
+                    *(u32x4*)d = u32x4{as_u32(y[0]), as_u32(y[1]), as_u32(y[2]), as_u32(y[3])};
+                } else {
+                    *(u32x2*)d = u32x2{(uint32_t)Elem<kType>::down(y[0]) | ((uint32_t)Elem<kType>::down(y[1]) << 16),
+                                       (uint32_t)Elem<kType>::down(y[2]) | ((uint32_t)Elem<kType>::down(y[3]) << 16)};
+                }
+            }
+        // the strip is this wave's own: its writes come before its reads
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int q = 0; q < 32 * kWords / kWave; ++q) {
+            const int at = q * kWave + lane, row = at / kWords, word = at % kWords;
+            const u32x4 v = *(const u32x4*)(strip + row * kRowBytes + word * 16);
+            const int64_t i = mf + row, j = nw + word * E;
+            if (i < m && j < n) store_vec<kType>(out + i * out_stride + nw, word, n - nw, v);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// ---- the product: few tokens ------------------------------------------------------
+
+// Up to 16 MT tokens: the weights are read once, straight into registers, at
+// the rate of HBM, and the tokens come from the caches.  A block takes 16
+// output channels, its 8 waves a share of the row each (v_mfma_i32_16x16x64_i8:
+// lane l holds 16 codes of channel or token l % 16), and adds their integer
+// sums up in LDS.
+constexpr int kSkinnyWaves = 8;
+
+template <int kType, int MT>
+__global__ __launch_bounds__(kSkinnyWaves * kWave) void skinny_kernel(
+    const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
+    const typename Elem<kType>::T* bias, int m, int64_t n, int32_t ld,
+    typename Elem<kType>::T* out, int64_t out_stride) {
+    __shared__ int sums[kSkinnyWaves][MT][16][17];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t wr = min(n0 + (lane & 15), n - 1);
+    const int8_t* w = b + wr * ld + (lane >> 4) * 16;
+    const int8_t* x[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) x[t] = a + (int64_t)min(t * 16 + (lane & 15), m - 1) * ld + (lane >> 4) * 16;
+    i32x4 acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = i32x4{0, 0, 0, 0};
+    const int lines = ld / 128;                  // of a row, shared out over the waves
+    int k = lines * wave / kSkinnyWaves * 128;
+    const int end = lines * (wave + 1) / kSkinnyWaves * 128;
+    auto some = [&](auto count) {                // `count` lines, all their loads in flight
+        constexpr int L = decltype(count)::value * 2;
+        i32x4 wv[L];
+#pragma unroll
+        for (int i = 0; i < L; ++i) wv[i] = *(const i32x4*)(w + k + i * 64);
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[i], *(const i32x4*)(x[t] + k + i * 64), acc[t], 0, 0, 0);
+        k += L * 64;
+    };
+    while (k + 4 * 128 <= end) some(std::integral_constant<int, 4>());
+    while (k < end) some(std::integral_constant<int, 1>());
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sums[wave][t][lane & 15][(lane >> 4) * 4 + r] = acc[t][r];
+    __syncthreads();
+    for (int q = threadIdx.x; q < MT * 256; q += kSkinnyWaves * kWave) {
+        const int t = q / 256, i = q % 256 / 16, j = q % 16;
+        if (t * 16 + i >= m || n0 + j >= n) continue;
+        int sum = 0;
+#pragma unroll
+        for (int v = 0; v < kSkinnyWaves; ++v) sum += sums[v][t][i][j];
+        float y = (float)sum * (a_scale[t * 16 + i] * b_scale[n0 + j]);
+        if (bias) y += Elem<kType>::up(bias[n0 + j]);
+        out[(int64_t)(t * 16 + i) * out_stride + n0 + j] = Elem<kType>::down(y);
     }
 }
 
@@ -161,15 +405,41 @@ static int launch_quantize(const void* x, int32_t type, int64_t rows, int64_t co
     });
 }
 
+template <int kType, int FN, int FM, int WN, int WM>
+static void launch_tile(const int8_t* a, const float* a_scale, const int8_t* b,
+                        const float* b_scale, const typename Elem<kType>::T* bias, int64_t m,
+                        int64_t n, int64_t ld, typename Elem<kType>::T* out, int64_t out_stride,
+                        hipStream_t st) {
+    typedef Tile<kType, FN, FM, WN, WM> S;
+    const int64_t tn = (n + S::BN - 1) / S::BN, tm = (m + S::BM - 1) / S::BM;
+    hipLaunchKernelGGL((tile_kernel<kType, FN, FM, WN, WM>), dim3((unsigned)(tn * tm)),
+                       dim3(S::kThreads), S::kLds, st, a, a_scale, b, b_scale, bias, m, n,
+                       (int32_t)ld, (uint32_t)tn, (uint32_t)tm, out, out_stride);
+}
+
 static int launch_matmul(const int8_t* a, const float* a_scale, const int8_t* b,
                          const float* b_scale, const void* bias, int64_t m, int64_t n, int64_t k,
                          void* out, int32_t type, int64_t out_stride, hipStream_t st) {
     return by_type(type, [&](auto t) {
         constexpr int kType = decltype(t)::value;
         typedef typename Elem<kType>::T T;
-        const dim3 grid((unsigned)((n + 63) / 64), (unsigned)((m + 15) / 16));
-        hipLaunchKernelGGL((matmul_kernel<kType>), grid, dim3(kBlock), 0, st, a, a_scale, b,
-                           b_scale, (const T*)bias, m, n, ld_of(k), (T*)out, out_stride);
+        const int64_t ld = ld_of(k);
+        const T* bi = (const T*)bias;
+        T* o = (T*)out;
+        const dim3 strips((unsigned)((n + 15) / 16)), threads(kSkinnyWaves * kWave);
+        if (m <= 16)
+            hipLaunchKernelGGL((skinny_kernel<kType, 1>), strips, threads, 0, st, a, a_scale, b,
+                               b_scale, bi, (int)m, n, (int32_t)ld, o, out_stride);
+        else if (m <= 32)
+            hipLaunchKernelGGL((skinny_kernel<kType, 2>), strips, threads, 0, st, a, a_scale, b,
+                               b_scale, bi, (int)m, n, (int32_t)ld, o, out_stride);
+        else if (m <= 64)
+            hipLaunchKernelGGL((skinny_kernel<kType, 4>), strips, threads, 0, st, a, a_scale, b,
+                               b_scale, bi, (int)m, n, (int32_t)ld, o, out_stride);
+        else if (((n + 255) / 256) * ((m + 255) / 256) < 200)
+            launch_tile<kType, 2, 2, 2, 2>(a, a_scale, b, b_scale, bi, m, n, ld, o, out_stride, st);
+        else
+            launch_tile<kType, 4, 4, 2, 2>(a, a_scale, b, b_scale, bi, m, n, ld, o, out_stride, st);
     });
 }
 
