@@ -792,7 +792,8 @@ static int check_grad(const void* grad, int32_t type, int64_t vocab, int64_t gra
 }
 
 static int check_workspace(const void* workspace, size_t have, size_t need) {
-    if (!workspace && need) return FLASHOPT_ERR_NULL;
+    if (need == 0) return FLASHOPT_OK;
+    if (!workspace) return FLASHOPT_ERR_NULL;
     if (have < need || !aligned(workspace, 256)) return FLASHOPT_ERR_WORKSPACE;
     return FLASHOPT_OK;
 }
@@ -833,7 +834,9 @@ static Cut cut_rows(int32_t type, int64_t rows, int64_t vocab) {
     return k;
 }
 
+// a row that one block holds needs no workspace
 static size_t parts_bytes(const Cut& k, int64_t rows) {
+    if (k.nseg == 1) return 0;
     const size_t b = (size_t)(rows * k.nseg) * sizeof(Part);
     return (b + 255) & ~size_t(255);
 }
@@ -981,6 +984,7 @@ size_t flashopt_logprob_workspace_bytes(int32_t type, int64_t rows, int64_t voca
         top > FLASHOPT_TOP_MAX || rows > INT32_MAX / ((vocab + 4095) / 4096))
         return 0;
     const Cut k = cut_rows(type, rows, vocab);
+    if (k.nseg == 1) return 0;
     return parts_bytes(k, rows) + (size_t)(rows * k.nseg) * (size_t)top * sizeof(uint64_t);
 }
 

@@ -769,33 +769,39 @@ def _arg(t: Optional[torch.Tensor], dtype, numel: int, device, name: str):
     if t is None:
         return None
     if t.dtype != dtype or t.numel() != numel or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements on {device}")
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements on "
+                         f"{device}")
     return t.data_ptr()
 
 
-def _scratch(workspace, need: int, device):
+def _scratch(workspace, need: int, device, stream):
+    """(address, bytes) of the workspace given or a new one, and what keeps it alive."""
     if workspace is None:
+        if need == 0:
+            return None, 0, None
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if stream is not None:               # not to be reused before that stream is done with it
+            workspace.record_stream(stream)
     elif workspace.dtype != torch.uint8 or workspace.device != device or \
             not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
-    return workspace
+    return workspace.data_ptr(), workspace.numel(), workspace
 
 
 def _call(fn: str, device, stream, *args) -> None:
     """The C call with `device` current, on the stream given or the device's own."""
     if device.type != "cuda":
         raise ValueError("expected device tensors")
-    current = torch.cuda.current_device()
-    if device.index == current:
-        if stream is None:
-            stream = torch.cuda.current_stream()
-        status = getattr(lib(), fn)(*args, stream.cuda_stream)
-    else:
+    if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
-            if stream is None:
-                stream = torch.cuda.current_stream()
-            status = getattr(lib(), fn)(*args, stream.cuda_stream)
+            _call(fn, device, stream, *args)
+        return
+    if stream is None:
+        # the current stream's handle, without building a Stream around it (2.7 us)
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        handle = stream.cuda_stream
+    status = getattr(lib(), fn)(*args, handle)
     if status != 0:
         raise FlashoptError(fn, status)
 
@@ -823,9 +829,10 @@ def flashopt_logprob(logits, targets=None, top: int = 0, temperature: float = 1.
     top] int64."""
     x, ty, rows, vocab, stride = _logits(logits)
     dev = logits.device
-    ws = _scratch(workspace, lib().flashopt_logprob_workspace_bytes(ty, rows, vocab, top), dev)
+    need = lib().flashopt_logprob_workspace_bytes(ty, rows, vocab, top)
+    wp, wb, _ws = _scratch(workspace, need, dev, stream)
     _call("flashopt_logprob", dev, stream, x, ty, rows, vocab, stride, temperature,
-          _arg(targets, torch.int64, rows, dev, "targets"), top, ws.data_ptr(), ws.numel(),
+          _arg(targets, torch.int64, rows, dev, "targets"), top, wp, wb,
           _arg(logprob, torch.float32, rows, dev, "logprob"),
           _arg(entropy, torch.float32, rows, dev, "entropy"),
           _arg(stats, torch.float32, 4 * rows, dev, "stats"),
@@ -851,11 +858,12 @@ def flashopt_logprob_grad(logits, targets, grad_logprob, grad_entropy, stats, gr
     x, ty, rows, vocab, stride = _logits(logits)
     dev = logits.device
     g, gs = _gradient(grad, logits)
-    ws = _scratch(workspace, lib().flashopt_logprob_workspace_bytes(ty, rows, vocab, 0), dev)
+    need = lib().flashopt_logprob_workspace_bytes(ty, rows, vocab, 0)
+    wp, wb, _ws = _scratch(workspace, need, dev, stream)
     _call("flashopt_logprob_grad", dev, stream, x, ty, rows, vocab, stride, temperature,
           _arg(targets, torch.int64, rows, dev, "targets"),
           _arg(grad_logprob, torch.float32, rows, dev, "grad_logprob"),
-          _arg(grad_entropy, torch.float32, rows, dev, "grad_entropy"), ws.data_ptr(), ws.numel(),
+          _arg(grad_entropy, torch.float32, rows, dev, "grad_entropy"), wp, wb,
           _arg(logprob, torch.float32, rows, dev, "logprob"),
           _arg(entropy, torch.float32, rows, dev, "entropy"),
           _arg(stats, torch.float32, 4 * rows, dev, "stats"), g, gs)
@@ -874,9 +882,10 @@ def flashopt_distill(logits, top_id, top_logprob, loss, stats, tail: bool = True
     x, ty, rows, vocab, stride = _logits(logits)
     dev = logits.device
     ids, tlp, top = _listed(top_id, top_logprob, rows, dev)
-    ws = _scratch(workspace, lib().flashopt_distill_workspace_bytes(ty, rows, vocab), dev)
+    need = lib().flashopt_distill_workspace_bytes(ty, rows, vocab)
+    wp, wb, _ws = _scratch(workspace, need, dev, stream)
     _call("flashopt_distill", dev, stream, x, ty, rows, vocab, stride, temperature, ids, tlp, top,
-          int(tail), ws.data_ptr(), ws.numel(), _arg(loss, torch.float32, rows, dev, "loss"),
+          int(tail), wp, wb, _arg(loss, torch.float32, rows, dev, "loss"),
           _arg(stats, torch.float32, 8 * rows, dev, "stats"))
 
 
@@ -898,10 +907,11 @@ def flashopt_distill_grad(logits, top_id, top_logprob, grad_loss, loss, stats, g
     dev = logits.device
     ids, tlp, top = _listed(top_id, top_logprob, rows, dev)
     g, gs = _gradient(grad, logits)
-    ws = _scratch(workspace, lib().flashopt_distill_workspace_bytes(ty, rows, vocab), dev)
+    need = lib().flashopt_distill_workspace_bytes(ty, rows, vocab)
+    wp, wb, _ws = _scratch(workspace, need, dev, stream)
     _call("flashopt_distill_grad", dev, stream, x, ty, rows, vocab, stride, temperature, ids, tlp,
-          top, int(tail), _arg(grad_loss, torch.float32, rows, dev, "grad_loss"), ws.data_ptr(),
-          ws.numel(), _arg(loss, torch.float32, rows, dev, "loss"),
+          top, int(tail), _arg(grad_loss, torch.float32, rows, dev, "grad_loss"), wp, wb,
+          _arg(loss, torch.float32, rows, dev, "loss"),
           _arg(stats, torch.float32, 8 * rows, dev, "stats"), g, gs)
 
 
@@ -931,11 +941,12 @@ def flashopt_int8_matmul(a, a_scale, b, b_scale, k: int, out, bias=None, workspa
     m, n = out.shape
     dev = out.device
     ld = lib().flashopt_int8_ld(k)
-    ws = _scratch(workspace, lib().flashopt_int8_workspace_bytes(m, n, k), dev)
+    need = lib().flashopt_int8_workspace_bytes(m, n, k)
+    wp, wb, _ws = _scratch(workspace, need, dev, stream)
     _call("flashopt_int8_matmul", dev, stream, _arg(a, torch.int8, m * ld, dev, "a"),
           _arg(a_scale, torch.float32, m, dev, "a_scale"), _arg(b, torch.int8, n * ld, dev, "b"),
           _arg(b_scale, torch.float32, n, dev, "b_scale"), _arg(bias, out.dtype, n, dev, "bias"),
-          m, n, k, out.data_ptr(), element_type(out), row_stride(out), ws.data_ptr(), ws.numel())
+          m, n, k, out.data_ptr(), element_type(out), row_stride(out), wp, wb)
 
 
 def flashopt_int8_linear(x, w, w_scale, out, bias=None, workspace=None, stream=None) -> None:
@@ -945,8 +956,9 @@ def flashopt_int8_linear(x, w, w_scale, out, bias=None, workspace=None, stream=N
     if out.shape[0] != m or out.dtype != x.dtype or x.device != dev:
         raise ValueError("x and out must have the same rows, type and device")
     ld = lib().flashopt_int8_ld(k)
-    ws = _scratch(workspace, lib().flashopt_int8_workspace_bytes(m, n, k), dev)
+    need = lib().flashopt_int8_workspace_bytes(m, n, k)
+    wp, wb, _ws = _scratch(workspace, need, dev, stream)
     _call("flashopt_int8_linear", dev, stream, x.data_ptr(), element_type(x), m, k, row_stride(x),
           _arg(w, torch.int8, n * ld, dev, "w"), _arg(w_scale, torch.float32, n, dev, "w_scale"),
           _arg(bias, out.dtype, n, dev, "bias"), n, out.data_ptr(), row_stride(out),
-          ws.data_ptr(), ws.numel())
+          wp, wb)

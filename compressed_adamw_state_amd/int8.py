@@ -79,26 +79,40 @@ def int8_linear(x: torch.Tensor, weight: Int8Weight, bias: Optional[torch.Tensor
     """y[..., n] = x[..., k] W^T + bias in x's type: x rounded to 8 bits per
     token, an exact integer product, the scales and the bias in FP32, one
     rounding."""
-    if x.shape[-1] != weight.k:
-        raise ValueError(f"x has {x.shape[-1]} features, the weight {weight.k}")
+    k, n, dev = weight.k, weight.n, weight.codes.device
+    if x.shape[-1] != k:
+        raise ValueError(f"x has {x.shape[-1]} features, the weight {k}")
     if x.requires_grad and torch.is_grad_enabled():
         raise ValueError("int8_linear has no gradient: call it under torch.no_grad()")
-    if x.device != weight.codes.device:
-        raise ValueError("x and the weight must be on one device")
-    if x.dim() == 2:
-        rows = x
-    else:
-        try:
-            rows = x.view(-1, weight.k)
-        except RuntimeError:
-            raise ValueError("x's leading dimensions must flatten without a copy") from None
+    if x.device != dev or not x.is_cuda:
+        raise ValueError("x and the weight must be on one GPU")
+    shape = x.shape[:-1] + (n,)
     if out is None:
-        out = torch.empty(x.shape[:-1] + (weight.n,), dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape[:-1] + (weight.n,) or out.dtype != x.dtype:
-        raise ValueError("out must have x's leading dimensions and type, and n features")
-    F.flashopt_int8_linear(rows, weight.codes, weight.scale,
-                           out if out.dim() == 2 else out.view(-1, weight.n), bias)
+        out = torch.empty(shape, dtype=x.dtype, device=dev)
+    elif out.shape != shape or out.dtype != x.dtype or out.device != dev:
+        raise ValueError("out must have x's leading dimensions, type and device, and n features")
+    if bias is not None and (bias.dtype != x.dtype or bias.shape != (n,) or bias.device != dev
+                             or not bias.is_contiguous()):
+        raise ValueError("bias must hold n values of x's type on its device")
+    rows, to = _matrix(x, k, "x"), _matrix(out, n, "out")
+    m = rows.shape[0]
+    need = F.lib().flashopt_int8_workspace_bytes(m, n, k)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    # the weight's arrays were checked when it was made
+    F._call("flashopt_int8_linear", dev, None, rows.data_ptr(), F.element_type(x), m, k,
+            F.row_stride(rows), weight.codes.data_ptr(), weight.scale.data_ptr(),
+            None if bias is None else bias.data_ptr(), n, to.data_ptr(), F.row_stride(to),
+            None if ws is None else ws.data_ptr(), need)
     return out
+
+
+def _matrix(t: torch.Tensor, cols: int, name: str) -> torch.Tensor:
+    if t.dim() == 2:
+        return t
+    try:
+        return t.view(-1, cols)
+    except RuntimeError:
+        raise ValueError(f"{name}'s leading dimensions must flatten without a copy") from None
 
 
 class Int8Linear(torch.nn.Module):

@@ -58,9 +58,9 @@ def _rows(logits: torch.Tensor) -> torch.Tensor:
         raise ValueError("the logits' leading dimensions must flatten without a copy") from None
 
 
-def _per_row(t: torch.Tensor, logits: torch.Tensor, dtype, name: str, last=()) -> torch.Tensor:
-    if t.dtype != dtype or t.shape != logits.shape[:-1] + tuple(last):
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(logits.shape[:-1]) + tuple(last)}")
+def _per_row(t: torch.Tensor, shape, device, dtype, name: str) -> torch.Tensor:
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {device}")
     return t if t.is_contiguous() else t.contiguous()
 
 
@@ -72,27 +72,48 @@ def _check_temperature(temperature: float) -> float:
 
 
 def _upstream(g: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
-    return None if g is None else g.to(torch.float32).contiguous()
+    if g is None:
+        return None
+    if g.dtype != torch.float32:
+        g = g.float()
+    return g if g.is_contiguous() else g.contiguous()
 
 
-def _forward(logits, targets, top, temperature, keep):
-    x = _rows(logits)
-    lead, dev = logits.shape[:-1], logits.device
-    logprob = None if targets is None else torch.empty(lead, dtype=torch.float32, device=dev)
-    entropy = torch.empty(lead, dtype=torch.float32, device=dev)
-    stats = torch.empty((x.shape[0], 4), dtype=torch.float32, device=dev) if keep else None
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _empty(shape, device, dtype=torch.float32) -> torch.Tensor:
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(need: int, device) -> Optional[torch.Tensor]:
+    return _empty(need, device, torch.uint8) if need else None
+
+
+# Below, the library is called with the addresses of tensors that the checks
+# above have seen or that were just made here.
+
+def _forward(logits, lead, targets, top, temperature, keep):
+    x, ty, rows, vocab, stride = F._logits(_rows(logits))
+    dev = logits.device
+    logprob = None if targets is None else _empty(lead, dev)
+    entropy = _empty(lead, dev)
+    stats = _empty((rows, 4), dev) if keep else None
     tl = ti = None
     if top:
-        tl = torch.empty(lead + (top,), dtype=torch.float32, device=dev)
-        ti = torch.empty(lead + (top,), dtype=torch.int64, device=dev)
-    F.flashopt_logprob(x, targets, top, temperature, logprob, entropy, stats, tl, ti)
+        tl, ti = _empty(lead + (top,), dev), _empty(lead + (top,), dev, torch.int64)
+    need = F.lib().flashopt_logprob_workspace_bytes(ty, rows, vocab, top)
+    ws = _workspace(need, dev)
+    F._call("flashopt_logprob", dev, None, x, ty, rows, vocab, stride, temperature, _at(targets),
+            top, _at(ws), need, _at(logprob), entropy.data_ptr(), _at(stats), _at(tl), _at(ti))
     return logprob, entropy, stats, tl, ti
 
 
 class _Logprob(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, targets, top, temperature):
-        logprob, entropy, stats, tl, ti = _forward(logits, targets, top, temperature, True)
+    def forward(ctx, logits, lead, targets, top, temperature):
+        logprob, entropy, stats, tl, ti = _forward(logits, lead, targets, top, temperature, True)
         ctx.save_for_backward(logits, targets, stats)
         ctx.temperature = temperature
         ctx.set_materialize_grads(False)
@@ -105,11 +126,15 @@ class _Logprob(torch.autograd.Function):
     def backward(ctx, g_logprob, g_entropy, _tl, _ti):
         logits, targets, stats = ctx.saved_tensors
         if g_logprob is None and g_entropy is None:
-            return None, None, None, None
-        grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        F.flashopt_logprob_backward(_rows(logits), targets, stats, _upstream(g_logprob),
-                                    _upstream(g_entropy), _rows(grad), ctx.temperature)
-        return grad, None, None, None
+            return None, None, None, None, None
+        g_logprob, g_entropy = _upstream(g_logprob), _upstream(g_entropy)
+        x, ty, rows, vocab, stride = F._logits(_rows(logits))
+        dev = logits.device
+        grad = _empty(logits.shape, dev, logits.dtype)
+        F._call("flashopt_logprob_backward", dev, None, x, ty, rows, vocab, stride,
+                ctx.temperature, _at(targets), stats.data_ptr(), _at(g_logprob), _at(g_entropy),
+                grad.data_ptr(), vocab)
+        return grad, None, None, None, None
 
 
 def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, top: int = 0,
@@ -119,49 +144,64 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     the `top` most likely tokens (0 to 64; equal logits by lowest id), of
     softmax(logits / temperature).  logprob and entropy are differentiable."""
     temperature = _check_temperature(temperature)
-    if not 0 <= top <= min(F.TOP_MAX, logits.shape[-1]):
+    if top < 0 or top > F.TOP_MAX or top > logits.shape[-1]:
         raise ValueError(f"top = {top} is outside 0 .. {min(F.TOP_MAX, logits.shape[-1])}")
+    lead = logits.shape[:-1]
     if targets is not None:
-        targets = _per_row(targets, logits, torch.int64, "targets")
-    if torch.is_grad_enabled() and logits.requires_grad:
-        return TokenLogprobs(*_Logprob.apply(logits, targets, top, temperature))
-    logprob, entropy, _, tl, ti = _forward(logits, targets, top, temperature, False)
+        targets = _per_row(targets, lead, logits.device, torch.int64, "targets")
+    if logits.requires_grad and torch.is_grad_enabled():
+        return TokenLogprobs(*_Logprob.apply(logits, lead, targets, top, temperature))
+    logprob, entropy, _, tl, ti = _forward(logits, lead, targets, top, temperature, False)
     return TokenLogprobs(logprob, entropy, tl, ti)
 
 
-def _grad_buffer(logits: torch.Tensor, inplace: bool) -> torch.Tensor:
+def _grad_buffer(logits: torch.Tensor, inplace: bool):
+    """(the gradient, its row stride)"""
     if inplace:
-        return logits.detach()
-    return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        return logits.detach(), F.row_stride(_rows(logits))
+    return _empty(logits.shape, logits.device, logits.dtype), logits.shape[-1]
 
 
-@torch.no_grad()
 def token_logprobs_grad(logits: torch.Tensor, targets: torch.Tensor, grad_logprob: torch.Tensor,
                         grad_entropy: Optional[torch.Tensor] = None, temperature: float = 1.0,
                         inplace: bool = False) -> TokenLogprobsGrad:
     """logprob, entropy and the gradient of sum(grad_logprob * logprob +
     grad_entropy * entropy) with respect to the logits (grad_*: FP32, one per
-    row)."""
+    row).  inplace: the gradient takes the logits' place, whose values nothing
+    else may need any more."""
     temperature = _check_temperature(temperature)
-    targets = _per_row(targets, logits, torch.int64, "targets")
-    grad_logprob = _per_row(grad_logprob, logits, torch.float32, "grad_logprob")
-    if grad_entropy is not None:
-        grad_entropy = _per_row(grad_entropy, logits, torch.float32, "grad_entropy")
-    x = _rows(logits)
     lead, dev = logits.shape[:-1], logits.device
-    logprob = torch.empty(lead, dtype=torch.float32, device=dev)
-    entropy = torch.empty(lead, dtype=torch.float32, device=dev)
-    stats = torch.empty((x.shape[0], 4), dtype=torch.float32, device=dev)
-    grad = _grad_buffer(logits, inplace)
-    F.flashopt_logprob_grad(x, targets, grad_logprob, grad_entropy, stats, _rows(grad), logprob,
-                            entropy, temperature)
+    targets = _per_row(targets, lead, dev, torch.int64, "targets")
+    grad_logprob = _per_row(grad_logprob, lead, dev, torch.float32, "grad_logprob")
+    if grad_entropy is not None:
+        grad_entropy = _per_row(grad_entropy, lead, dev, torch.float32, "grad_entropy")
+    x, ty, rows, vocab, stride = F._logits(_rows(logits))
+    logprob, entropy, stats = _empty(lead, dev), _empty(lead, dev), _empty((rows, 4), dev)
+    grad, grad_stride = _grad_buffer(logits, inplace)
+    need = F.lib().flashopt_logprob_workspace_bytes(ty, rows, vocab, 0)
+    ws = _workspace(need, dev)
+    F._call("flashopt_logprob_grad", dev, None, x, ty, rows, vocab, stride, temperature,
+            targets.data_ptr(), grad_logprob.data_ptr(), _at(grad_entropy), _at(ws), need,
+            logprob.data_ptr(), entropy.data_ptr(), stats.data_ptr(), grad.data_ptr(), grad_stride)
     return TokenLogprobsGrad(logprob, entropy, grad)
+
+
+def _distill_forward(logits, lead, top_id, top_logprob, tail, temperature):
+    x, ty, rows, vocab, stride = F._logits(_rows(logits))
+    dev = logits.device
+    loss, stats = _empty(lead, dev), _empty((rows, 8), dev)
+    need = F.lib().flashopt_distill_workspace_bytes(ty, rows, vocab)
+    ws = _workspace(need, dev)
+    F._call("flashopt_distill", dev, None, x, ty, rows, vocab, stride, temperature,
+            top_id.data_ptr(), top_logprob.data_ptr(), top_id.shape[-1], tail, _at(ws), need,
+            loss.data_ptr(), stats.data_ptr())
+    return loss, stats
 
 
 class _Distill(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, top_id, top_logprob, tail, temperature):
-        loss, stats = _distill_forward(logits, top_id, top_logprob, tail, temperature)
+    def forward(ctx, logits, lead, top_id, top_logprob, tail, temperature):
+        loss, stats = _distill_forward(logits, lead, top_id, top_logprob, tail, temperature)
         ctx.save_for_backward(logits, top_id, top_logprob, stats)
         ctx.temperature = temperature
         return loss
@@ -170,30 +210,25 @@ class _Distill(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, g):
         logits, top_id, top_logprob, stats = ctx.saved_tensors
-        grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        top = top_id.shape[-1]
-        F.flashopt_distill_backward(_rows(logits), top_id.view(-1, top), top_logprob.view(-1, top),
-                                    stats, _upstream(g), _rows(grad), ctx.temperature)
-        return grad, None, None, None, None
+        g = _upstream(g)
+        x, ty, rows, vocab, stride = F._logits(_rows(logits))
+        dev = logits.device
+        grad = _empty(logits.shape, dev, logits.dtype)
+        F._call("flashopt_distill_backward", dev, None, x, ty, rows, vocab, stride,
+                ctx.temperature, top_id.data_ptr(), top_logprob.data_ptr(), top_id.shape[-1],
+                stats.data_ptr(), g.data_ptr(), grad.data_ptr(), vocab)
+        return grad, None, None, None, None, None
 
 
-def _distill_forward(logits, top_id, top_logprob, tail, temperature):
-    x, top = _rows(logits), top_id.shape[-1]
-    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)
-    stats = torch.empty((x.shape[0], 8), dtype=torch.float32, device=logits.device)
-    F.flashopt_distill(x, top_id.view(-1, top), top_logprob.view(-1, top), loss, stats, tail,
-                       temperature)
-    return loss, stats
-
-
-def _teacher(logits, top_id, top_logprob):
+def _teacher(logits, lead, top_id, top_logprob):
     top = top_id.shape[-1] if top_id.dim() else 0
-    if not 1 <= top <= min(F.TOP_MAX, logits.shape[-1]):
+    if top < 1 or top > F.TOP_MAX or top > logits.shape[-1]:
         raise ValueError(f"{top} alternatives are outside 1 .. {min(F.TOP_MAX, logits.shape[-1])}")
     if top_logprob.requires_grad and torch.is_grad_enabled():
         raise ValueError("the teacher's log probabilities have no gradient here: detach them")
-    return (_per_row(top_id, logits, torch.int64, "top_id", (top,)),
-            _per_row(top_logprob, logits, torch.float32, "top_logprob", (top,)))
+    shape = lead + (top,)
+    return (_per_row(top_id, shape, logits.device, torch.int64, "top_id"),
+            _per_row(top_logprob, shape, logits.device, torch.float32, "top_logprob"))
 
 
 def distill_loss(logits: torch.Tensor, top_id: torch.Tensor, top_logprob: torch.Tensor,
@@ -205,25 +240,29 @@ def distill_loss(logits: torch.Tensor, top_id: torch.Tensor, top_logprob: torch.
     whole.  Differentiable in the logits; multiply by temperature ** 2 for
     the customary weight."""
     temperature = _check_temperature(temperature)
-    top_id, top_logprob = _teacher(logits, top_id, top_logprob)
-    if torch.is_grad_enabled() and logits.requires_grad:
-        return _Distill.apply(logits, top_id, top_logprob, bool(tail), temperature)
-    return _distill_forward(logits, top_id, top_logprob, bool(tail), temperature)[0]
+    lead = logits.shape[:-1]
+    top_id, top_logprob = _teacher(logits, lead, top_id, top_logprob)
+    if logits.requires_grad and torch.is_grad_enabled():
+        return _Distill.apply(logits, lead, top_id, top_logprob, bool(tail), temperature)
+    return _distill_forward(logits, lead, top_id, top_logprob, bool(tail), temperature)[0]
 
 
-@torch.no_grad()
 def distill_grad(logits: torch.Tensor, top_id: torch.Tensor, top_logprob: torch.Tensor,
                  grad_loss: torch.Tensor, tail: bool = True, temperature: float = 1.0,
                  inplace: bool = False):
     """(loss, gradient of sum(grad_loss * loss) with respect to the logits);
-    grad_loss: FP32, one per row."""
+    grad_loss: FP32, one per row; inplace as in token_logprobs_grad."""
     temperature = _check_temperature(temperature)
-    top_id, top_logprob = _teacher(logits, top_id, top_logprob)
-    grad_loss = _per_row(grad_loss, logits, torch.float32, "grad_loss")
-    x, top = _rows(logits), top_id.shape[-1]
-    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)
-    stats = torch.empty((x.shape[0], 8), dtype=torch.float32, device=logits.device)
-    grad = _grad_buffer(logits, inplace)
-    F.flashopt_distill_grad(x, top_id.view(-1, top), top_logprob.view(-1, top), grad_loss, loss,
-                            stats, _rows(grad), bool(tail), temperature)
+    lead, dev = logits.shape[:-1], logits.device
+    top_id, top_logprob = _teacher(logits, lead, top_id, top_logprob)
+    grad_loss = _per_row(grad_loss, lead, dev, torch.float32, "grad_loss")
+    x, ty, rows, vocab, stride = F._logits(_rows(logits))
+    loss, stats = _empty(lead, dev), _empty((rows, 8), dev)
+    grad, grad_stride = _grad_buffer(logits, inplace)
+    need = F.lib().flashopt_distill_workspace_bytes(ty, rows, vocab)
+    ws = _workspace(need, dev)
+    F._call("flashopt_distill_grad", dev, None, x, ty, rows, vocab, stride, temperature,
+            top_id.data_ptr(), top_logprob.data_ptr(), top_id.shape[-1], bool(tail),
+            grad_loss.data_ptr(), _at(ws), need, loss.data_ptr(), stats.data_ptr(),
+            grad.data_ptr(), grad_stride)
     return loss, grad

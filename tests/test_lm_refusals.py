@@ -35,12 +35,14 @@ def test_logprob_refusals():
     assert logprob(targets=None) == -1 and logprob(targets=P(0x10004)) == -3
     assert logprob(st=P(0x10008)) == -3 and logprob(lp=P(0x10002)) == -3 and logprob(en=ODD) == -3
     assert logprob(top=1, tl=ODD, ti=A) == -3 and logprob(top=1, tl=A, ti=P(0x10004)) == -3
-    need = F.lib().flashopt_logprob_workspace_bytes(BF16, 4, 100, 0)
-    assert need > 0 and logprob(wsb=need - 1) == -6 and logprob(ws=P(0x10010)) == -6 and logprob(ws=None) == -1
+    big = dict(vocab=100000, stride=100000)
+    need = F.lib().flashopt_logprob_workspace_bytes(BF16, 4, 100000, 0)
+    assert need > 0 and logprob(wsb=need - 1, **big) == -6
+    assert logprob(ws=P(0x10010), **big) == -6 and logprob(ws=None, **big) == -1
     assert F.lib().flashopt_logprob_workspace_bytes(9, 4, 100, 0) == 0
     assert F.lib().flashopt_logprob_workspace_bytes(BF16, 4, 100, 65) == 0
     assert F.lib().flashopt_logprob_workspace_bytes(BF16, -4, 100, 5) == 0
-    assert F.lib().flashopt_logprob_workspace_bytes(BF16, 4, 100, 5) >= need + 4 * 5 * 8
+    assert F.lib().flashopt_logprob_workspace_bytes(BF16, 4, 100000, 5) >= need + 4 * 5 * 8
 
 
 def test_logprob_gradient_refusals():
@@ -49,14 +51,14 @@ def test_logprob_gradient_refusals():
     assert back(rows=0) == 0 and back(grad=None) == -1 and back(st=None) == -1 and back(targets=None) == -1
     assert back(gs=99) == -2 and back(grad=ODD) == -3 and back(gl=P(0x10002)) == -3 and back(gh=ODD) == -3
 
-    def both(grad=A, gs=100, st=A, targets=A, gl=A, ws=A, wsb=1 << 20, lp=A):
-        return F.lib().flashopt_logprob_grad(A, BF16, 4, 100, 100, 1.0, targets, gl, None, ws, wsb, lp, A, st, grad, gs, None)
+    def both(grad=A, gs=100000, st=A, targets=A, gl=A, ws=A, wsb=1 << 20, lp=A):
+        return F.lib().flashopt_logprob_grad(A, BF16, 4, 100000, 100000, 1.0, targets, gl, None, ws, wsb, lp, A, st, grad, gs, None)
     assert both(grad=None) == -1 and both(st=None) == -1 and both(targets=None) == -1
     assert both(gs=99) == -2 and both(wsb=1) == -6 and both(ws=None) == -1 and both(st=P(0x10004)) == -3
 
 
 def test_distill_refusals():
-    def fwd(rows=4, vocab=100, ids=A, tlp=A, top=4, tail=1, ws=A, wsb=1 << 20, loss=A, st=A, temp=1.0):
+    def fwd(rows=4, vocab=100000, ids=A, tlp=A, top=4, tail=1, ws=A, wsb=1 << 20, loss=A, st=A, temp=1.0):
         return F.lib().flashopt_distill(A, BF16, rows, vocab, vocab, temp, ids, tlp, top, tail, ws, wsb, loss, st, None)
     assert fwd(rows=0) == 0 and fwd(top=0) == -4 and fwd(top=65) == -4 and fwd(vocab=3) == -4 and fwd(tail=2) == -4
     assert fwd(ids=None) == -1 and fwd(tlp=None) == -1 and fwd(st=None) == -1 and fwd(ws=None) == -1
@@ -69,7 +71,8 @@ def test_distill_refusals():
     assert back(gs=1) == -2 and back(top=0) == -4 and back(grad=ODD) == -3 and back(g=ODD) == -3
 
     def both(g=A, grad=A, wsb=1 << 20, top=4, tail=0):
-        return F.lib().flashopt_distill_grad(A, BF16, 4, 100, 100, 1.0, A, A, top, tail, g, A, wsb, A, A, grad, 100, None)
+        return F.lib().flashopt_distill_grad(A, BF16, 4, 100000, 100000, 1.0, A, A, top, tail, g, A, wsb, A, A, grad,
+                                             100000, None)
     assert both(g=None) == -1 and both(grad=None) == -1 and both(wsb=1) == -6 and both(top=0) == -4 and both(tail=-1) == -4
 
 
