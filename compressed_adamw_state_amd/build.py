@@ -21,9 +21,9 @@ CSRC = os.path.join(PKG, "csrc")
 # step that allocates nothing, and the language-model operators (losses over
 # rows of logits; rows in 8 bits and the linear layer over them)
 UNITS = ["step.hip", "step_fp32.hip", "tensor.hip", "ablation.hip", "probe.hip", "schedule.hip",
-         "list.hip", "noalloc.hip", "logits.hip", "int8.hip"]
+         "list.hip", "noalloc.hip", "logits.hip", "logits_row.hip", "int8.hip"]
 SOURCES = [os.path.join(CSRC, u) for u in UNITS] + [
-    os.path.join(CSRC, h) for h in ("codec.hpp", "device.hpp", "host.hpp", "quant.hpp", "rows.hpp")]
+    os.path.join(CSRC, h) for h in ("codec.hpp", "device.hpp", "host.hpp", "quant.hpp", "rows.hpp", "logits.hpp")]
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libflashopt.so")
 ARCH = os.environ.get("FLASHOPT_ARCH", "gfx950")

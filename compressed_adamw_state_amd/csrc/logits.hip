@@ -20,19 +20,15 @@
 // read before it, so that a gradient may replace its logits.
 #include <cmath>
 
-#include "rows.hpp"
+#include "logits.hpp"
 
 namespace flashopt {
 
 // 16-byte words of a chunk per thread: 8 streams best; with few rows 2 give
 // more, shorter work items.
 constexpr int kLong = 8, kShort = 2;
+constexpr int kMaxSegments = 64;                 // of a row: one wave joins them
 template <int kType, int kVecs> constexpr int kChunk = kVecs * kBlock * Elem<kType>::kE;
-
-// A part of a row: maximum of x, S, U.
-struct Part {
-    float m, s, u, pad;
-};
 
 // A row's order of entries as unsigned numbers: larger logit first, equal
 // ones by lowest id; a NaN ranks above all.
@@ -52,9 +48,16 @@ __device__ __forceinline__ uint64_t entry(float x, uint32_t id) {
 __device__ __forceinline__ uint32_t entry_id(uint64_t e) { return 0xFFFFFFFFu - (uint32_t)e; }
 __device__ __forceinline__ uint32_t entry_key(uint64_t e) { return (uint32_t)(e >> 32); }
 
+__device__ __forceinline__ void write_top(const ProbOut& o, int64_t row, int top, int k,
+                                          uint64_t e, float c, const ProbStats& st) {
+    o.top_id[row * top + k] = entry_id(e);
+    o.top_logprob[row * top + k] = ((key_value(entry_key(e)) - st.m) * c - st.l2s) * kLn2;
+}
+
+
 // A segment of a row: the words [begin, end) of 16 bytes; the row's last
-// word may be partial.
-template <int kType>
+// word may be partial.  Chunks are kVecs words of each of kThreads threads.
+template <int kType, int kThreads = kBlock>
 struct Segment {
     typedef typename Elem<kType>::T T;
     const T* x;
@@ -63,16 +66,16 @@ struct Segment {
 
     template <int kVecs>
     __device__ __forceinline__ void load(int64_t chunk, u32x4* r) const {
-        const int64_t v0 = begin + chunk * (kVecs * kBlock);
+        const int64_t v0 = begin + chunk * (kVecs * kThreads);
         if (whole<kVecs>(v0)) {                  // all loads in flight at once
             const T* p = x + v0 * Elem<kType>::kE;
 #pragma unroll
             for (int i = 0; i < kVecs; ++i)
-                r[i] = *reinterpret_cast<const u32x4_any*>(p + (threadIdx.x + i * kBlock) * Elem<kType>::kE);
+                r[i] = *reinterpret_cast<const u32x4_any*>(p + (threadIdx.x + i * kThreads) * Elem<kType>::kE);
         } else {
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                const int64_t w = v0 + threadIdx.x + i * kBlock;
+                const int64_t w = v0 + threadIdx.x + i * kThreads;
                 // words past the segment belong to another block, or to no row
                 r[i] = load_vec<kType>(x, w, w < end ? vocab : 0, Elem<kType>::kMinusInf);
             }
@@ -81,22 +84,22 @@ struct Segment {
     // a chunk of whole words, all of the segment (equal for the block's threads)
     template <int kVecs>
     __device__ __forceinline__ bool whole(int64_t v0) const {
-        const int64_t e = v0 + kVecs * kBlock;
+        const int64_t e = v0 + kVecs * kThreads;
         return e <= end && e * Elem<kType>::kE <= vocab;
     }
     template <int kVecs>
     __device__ __forceinline__ void store(T* g, int64_t chunk, int i, u32x4 o) const {
-        const int64_t v0 = begin + chunk * (kVecs * kBlock);
+        const int64_t v0 = begin + chunk * (kVecs * kThreads);
         if (whole<kVecs>(v0)) {
-            *reinterpret_cast<u32x4_any*>(g + v0 * Elem<kType>::kE + (threadIdx.x + i * kBlock) * Elem<kType>::kE) = o;
+            *reinterpret_cast<u32x4_any*>(g + v0 * Elem<kType>::kE + (threadIdx.x + i * kThreads) * Elem<kType>::kE) = o;
         } else {
-            const int64_t w = v0 + threadIdx.x + i * kBlock;
+            const int64_t w = v0 + threadIdx.x + i * kThreads;
             store_vec<kType>(g, w, w < end ? vocab : 0, o);
         }
     }
     template <int kVecs>
     __device__ __forceinline__ int chunks() const {
-        return (int)((end - begin + kVecs * kBlock - 1) / (kVecs * kBlock));
+        return (int)((end - begin + kVecs * kThreads - 1) / (kVecs * kThreads));
     }
     __device__ __forceinline__ int64_t first_id() const { return begin * Elem<kType>::kE; }
     __device__ __forceinline__ int64_t end_id() const {
@@ -261,184 +264,130 @@ __device__ __forceinline__ void segment_top(const Segment<kType>& seg, const flo
     if (threadIdx.x >= need && threadIdx.x < (uint32_t)top) out(threadIdx.x, uint64_t(0));
 }
 
-// ---- a row's numbers --------------------------------------------------------------
+// ---- sums ---------------------------------------------------------------------------
 
-// The row's part from its segments' (one wave; every lane gets it).
-__device__ __forceinline__ Part join_parts(const Part* part, int n, float c) {
-    const int lane = threadIdx.x & (kWave - 1);
-    float m = -INFINITY;
-    for (int k = lane; k < n; k += kWave) m = fmaxf(m, part[k].m);
-    m = wave_max(m);
-    float s = 0.0f, u = 0.0f;
-    for (int k = lane; k < n; k += kWave) {
-        const Part p = part[k];
-        if (p.m == -INFINITY && p.s == 0.0f) continue;           // an empty part
-        const float D = fmaxf((p.m - m) * c, -200.0f), f = exp2_hw(D);
-        s += p.s * f;
-        u += f * (p.u + D * p.s);
+// 2^((x - m) c - a) for many x: one fma and one exp2 where m c is small
+// enough, (x - m) formed first where it is not (beyond 2^20 the rounding of
+// m c, at most 2^-24 of it, would no longer be small as an exponent; entries
+// of the type's lowest value are there too).  What k = RN(m c + a) rounds away
+// is the same for all x: `left` = m c + a - k, to be taken off the exponent.
+struct Shift {
+    float m, c, a, k, left;
+    bool fast;
+    __device__ __forceinline__ Shift(float m_, float c_, float a_) : m(m_), c(c_), a(a_) {
+        const float hi = m * c, lo = __builtin_fmaf(m, c, -hi);
+        k = hi + a;
+        const float b = k - hi;
+        left = lo + ((hi - (k - b)) + (a - b));
+        fast = __builtin_fabsf(hi) < 0x1p20f;
     }
-    return Part{m, wave_sum(s), wave_sum(u), 0.0f};
-}
-
-// stats of a row for the gradient: shift m, log2 S, H, and whether the row has
-// a distribution (1 or 0).  One without keeps shift 0, so that its entries
-// give 2^(-inf) = 0.
-struct ProbStats {
-    float m, l2s, entropy, on;
+    template <bool kFast> __device__ __forceinline__ float exponent(float x) const {
+        return kFast ? __builtin_fmaf(x, c, -k) : (x - m) * c - a;
+    }
 };
 
-__device__ __forceinline__ ProbStats prob_stats(const Part& p) {
-    const bool empty = p.m == -INFINITY && p.s == 0.0f;
-    ProbStats st;
-    st.m = empty ? 0.0f : p.m;
-    st.l2s = empty ? 0.0f : log2_hw(p.s);
-    st.entropy = empty ? 0.0f : (st.l2s - p.u / p.s) * kLn2;
-    st.on = empty ? 0.0f : 1.0f;
-    return st;
+// S and U of N words relative to a shift that was chosen before them, and
+// their maximum (kTop).
+template <int kType, bool kU, bool kTop, bool kBound, int N>
+__device__ __forceinline__ void word_sums(const u32x4* r, const Shift& h, float& s, float& u,
+                                          float& top) {
+    constexpr int E = Elem<kType>::kE;
+    s = 0.0f;
+    u = 0.0f;
+    top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float x = Elem<kType>::get(r[i], e);
+            if (kTop) top = fmaxf(top, x);
+            const float d = h.exponent<true>(x);
+            const float p = exp2_hw(d);
+            s += p;
+            // where p is 0 the bound keeps 0 * -inf out of the sum
+            if (kU) u = __builtin_fmaf(p, kBound ? fmaxf(d, -200.0f) : d, u);
+        }
+        __builtin_amdgcn_sched_barrier(0);       // a word's values at a time in registers
+    }
 }
 
-struct ProbOut {                                 // each may be null
-    const int64_t* targets;
-    float *logprob, *entropy;
-    ProbStats* stats;
-    float* top_logprob;
-    int64_t* top_id;
+// A thread's running sums of its words.  The shift m is the maximum of the
+// first words that had one, so that later words need one pass only (a sum may
+// lie on either side of 1); it is raised when words exceed it by 2^24.  Words
+// of -inf alone, NaN, infinities and magnitudes beyond Shift's take the path
+// with a maximum of their own.
+template <int kType, bool kU, bool kTop>
+struct Sums {
+    float m, s, u, c, g;
+    bool bound;                                  // an entry of -inf was seen
+    Shift h;
+    __device__ __forceinline__ explicit Sums(float c_)
+        : m(-INFINITY), s(0.0f), u(0.0f), c(c_), g(1.0f), bound(false), h(-INFINITY, c_, 0.0f) {
+        h.fast = false;
+    }
+
+    // N words; returns their maximum (kTop)
+    template <int N>
+    __device__ __forceinline__ float add(u32x4* r) {
+        float top = -INFINITY;
+        if (h.fast) {
+            float cs, cu;
+            if (!kU || !bound) word_sums<kType, kU, kTop, false, N>(r, h, cs, cu, top);
+            if (kU && (bound || cu != cu)) {
+                bound = true;
+                hide<N>(r);
+                word_sums<kType, kU, kTop, true, N>(r, h, cs, cu, top);
+            }
+            if (cs < 0x1p24f) {
+                if (kU) u = __builtin_fmaf(g, cu - h.left * cs, u);
+                s = __builtin_fmaf(g, cs, s);
+                return top;
+            }
+        }
+        return slow<N>(r);
+    }
+
+    // keeps the compiler from holding a word's unpacked values for a later pass
+    template <int N> static __device__ __forceinline__ void hide(u32x4* r) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) asm volatile("" : "+v"(r[i]));
+    }
+    template <int N>
+    __device__ __forceinline__ float slow(u32x4* r) {
+        constexpr int E = Elem<kType>::kE;
+        hide<N>(r);
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < E; ++e) top = fmaxf(top, Elem<kType>::get(r[i], e));
+        hide<N>(r);
+        const float m_new = fmaxf(m, top);
+        // -inf: nothing yet, every p is 0
+        const float base = m_new == -INFINITY ? 0.0f : m_new;
+        float cs = 0.0f, cu = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float d = (Elem<kType>::get(r[i], e) - base) * c;
+                const float p = exp2_hw(d);
+                cs += p;
+                if (kU) cu = __builtin_fmaf(p, fmaxf(d, -200.0f), cu);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        const float D = fmaxf((m - m_new) * c, -200.0f), f = exp2_hw(D);
+        if (kU) u = f * (u + D * s) + cu;
+        s = s * f + cs;
+        m = m_new;
+        h = Shift(m, c, 0.0f);
+        g = exp2_hw(-h.left);
+        return top;
+    }
 };
 
-// one lane
-template <int kType>
-__device__ __forceinline__ void write_prob(const typename Elem<kType>::T* x, int64_t vocab,
-                                           int64_t row, float c, const ProbStats& st,
-                                           const ProbOut& o) {
-    if (o.entropy) o.entropy[row] = st.entropy;
-    if (o.stats) o.stats[row] = st;
-    if (o.logprob) {
-        const int64_t t = o.targets[row];
-        float lp = 0.0f;
-        if (t >= 0 && t < vocab) lp = ((Elem<kType>::up(x[t]) - st.m) * c - st.l2s) * kLn2;
-        o.logprob[row] = lp;
-    }
-}
-__device__ __forceinline__ void write_top(const ProbOut& o, int64_t row, int top, int k,
-                                          uint64_t e, float c, const ProbStats& st) {
-    o.top_id[row * top + k] = entry_id(e);
-    o.top_logprob[row * top + k] = ((key_value(entry_key(e)) - st.m) * c - st.l2s) * kLn2;
-}
-
-// stats of a row of distillation.  The gradient is
-//   outside the list: e_j coef, e_j = 2^((x_j - rest_m) c - rest_l2) the
-//                     entry's share of the rest, coef = (Q + r) P - r;
-//   in the list:      (Q + r) p_j - sum of its q, p_j from m and l2s;
-// q_k = 2^(t_k log2e - norm), all times g / T.  A row without a gradient has
-// on = 0.
-struct DistillStats {
-    float rest_m, rest_l2, coef, qr, m, l2s, norm, on;
-};
-
-struct DistillIn {
-    const int64_t* ids;
-    const float* tlp;
-    int top, tail;
-};
-
-// log2 of s as a whole number and the rest, which is then off by 2^-24 or so
-// whatever the size of s
-__device__ __forceinline__ void log2_parts(float s, float& whole, float& frac) {
-    const int e = __builtin_amdgcn_frexp_expf(s);
-    whole = (float)e;
-    frac = log2_hw(__builtin_amdgcn_ldexpf(s, -e));
-}
-// a * b as a rounded product and its rounding error, plus a * b_low
-__device__ __forceinline__ void product_parts(float a, float b, float b_low, float& hi, float& lo) {
-    hi = a * b;
-    lo = __builtin_fmaf(a, b, -hi) + a * b_low;
-}
-constexpr float kLog2eLow = 0x1.4ae0cp-26f;      // 1 / log 2 - kLog2e
-
-// q = 2^(t log2e - norm) with norm = whole + frac: the whole part goes into
-// the exponent, so that q is good to its last bits for small q too
-__device__ __forceinline__ float teacher_q(float t, float nwhole, float nfrac, float& hi, float& lo) {
-    product_parts(t, kLog2e, kLog2eLow, hi, lo);
-    if (!(hi > -300.0f)) { lo = 0.0f; return t != t ? t : 0.0f; }
-    const float n = __builtin_rintf(hi);
-    return __builtin_amdgcn_ldexpf(exp2_hw((hi - n) + (lo - nfrac)), (int)(n - nwhole));
-}
-
-// The row's loss and stats from the part of its unlisted entries (one wave).
-// The divergence is a difference of logarithms near 10 that may itself be
-// near 0: their whole parts are subtracted exactly.
-template <int kType>
-__device__ __forceinline__ DistillStats distill_stats(const typename Elem<kType>::T* x,
-                                                      int64_t vocab, int64_t row, float c,
-                                                      float c_low, const DistillIn& in,
-                                                      const Part& rest, float& loss) {
-    const int lane = threadIdx.x & (kWave - 1);
-    // lane k holds alternative k; a repeated id is summed into S once
-    const int64_t id = lane < in.top ? in.ids[row * in.top + lane] : -1;
-    const bool ok = id >= 0 && id < vocab;
-    const int own = ok ? (int)id : -1;
-    const float xk = ok ? Elem<kType>::up(x[id]) : -INFINITY;
-    const float t = ok ? in.tlp[row * in.top + lane] : -INFINITY;
-    bool first = ok;
-    for (int k = 0; k < in.top - 1; ++k) {
-        const int other = __builtin_amdgcn_readlane(own, k);
-        if (k < lane && other == own) first = false;
-    }
-    const float m0 = fmaxf(rest.m, wave_max(xk));
-    const bool no_rest = rest.m == -INFINITY && rest.s == 0.0f;
-    // the student's row has no distribution
-    const bool empty = m0 == -INFINITY && no_rest && __ballot(ok && xk != xk) == 0;
-    const float m = empty ? 0.0f : m0;
-    const float rest_f = no_rest ? 0.0f : exp2_hw(fmaxf((rest.m - m) * c, -200.0f));
-    const float s = wave_sum(first ? exp2_hw((xk - m) * c) : 0.0f) + (no_rest ? 0.0f : rest.s * rest_f);
-    float sw = 0.0f, sf = 0.0f, rw = 0.0f, rf = 0.0f;
-    if (!empty) log2_parts(s, sw, sf);
-    if (!no_rest) log2_parts(rest.s, rw, rf);
-    // the teacher's side
-    float nw = 0.0f, nf = 0.0f;
-    if (!in.tail) {
-        const float tm = wave_max(t);
-        const float ts = wave_sum(ok ? exp2_hw((t - tm) * kLog2e) : 0.0f);
-        float hi, lo, w, f;
-        product_parts(tm, kLog2e, kLog2eLow, hi, lo);
-        log2_parts(ts, w, f);
-        const float n = __builtin_rintf(hi);
-        nw = n + w;
-        nf = (hi - n) + (lo + f);
-    }
-    float hi, lo;
-    const float q = ok ? teacher_q(t, nw, nf, hi, lo) : 0.0f;
-    const float Q = wave_sum(q);
-    float r = in.tail ? fmaxf(0.0f, 1.0f - Q) : 0.0f;
-    if (no_rest) r = 0.0f;
-    // log2 q - log2 p
-    float term = 0.0f;
-    if (q > 0.0f) {
-        float ph, pl;
-        product_parts(xk - m, c, c_low, ph, pl);
-        if (!(ph > -3e38f)) pl = 0.0f;
-        term = q * (((hi - ph) + (sw - nw)) + ((lo - pl) + (sf - nf)));
-    } else if (q != 0.0f) {
-        term = q;                                // NaN
-    }
-    float sum = wave_sum(term);
-    const float rest_m = no_rest ? 0.0f : rest.m;
-    float dh, dl;
-    product_parts(rest_m - m, c, c_low, dh, dl);
-    if (!(dh > -3e38f)) dl = 0.0f;
-    if (r > 0.0f) {
-        float w, f;
-        log2_parts(r, w, f);
-        sum += r * (((w - rw) + sw - dh) + ((f - rf) + (sf - dl)));
-    }
-    const float P = no_rest ? 0.0f : exp2_hw((dh + (rw - sw)) + (dl + (rf - sf)));
-    const bool on = __ballot(ok) != 0 && !empty;
-    loss = on ? sum * kLn2 : 0.0f;
-    return DistillStats{rest_m, rw + rf, on ? (Q + r) * P - r : 0.0f, Q + r, m, sw + sf, nw + nf,
-                        on ? 1.0f : 0.0f};
-}
-
-// ---- gradients --------------------------------------------------------------------
+// ---- gradients ------------------------------------------------------------------------
 
 // grad_j = p_j (A + B d_j) with d_j = log2 p_j, plus gl at the given token.
 template <int kType>
@@ -448,49 +397,35 @@ struct ProbGrad {
     int64_t stride;
     float inv_t;
 };
-
-// One chunk of the gradient; target < 0: none.
-template <int kType, int kVecs, bool kEntropy>
-__device__ __forceinline__ void prob_grad_chunk(const Segment<kType>& seg, int ch, float c, float A,
-                                                float B, const ProbStats& st,
-                                                typename Elem<kType>::T* g) {
-    constexpr int E = Elem<kType>::kE;
-    u32x4 r[kVecs];
-    seg.template load<kVecs>(ch, r);
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        float o[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float d = (Elem<kType>::get(r[i], e) - st.m) * c - st.l2s;
-            const float p = exp2_hw(d);
-            o[e] = p * (kEntropy ? __builtin_fmaf(B, fmaxf(d, -200.0f), A) : A);
+template <bool kEntropy>
+struct ProbCoef {
+    Shift h;
+    float A, B, gl, low;
+    __device__ __forceinline__ ProbCoef(const ProbStats& st, float c, float gl_, float gh)
+        : h(st.m, c, st.l2s), gl(gl_) {
+        A = -gl - gh * st.entropy;
+        B = -gh * kLn2;
+        low = -200.0f;
+        if (h.fast) {                            // the exponent's constant part into the factors
+            const float g = exp2_hw(-h.left);
+            A = g * (A - B * h.left);
+            B = g * B;
         }
-        seg.template store<kVecs>(g, ch, i, pack<kType>(o));
     }
-}
-
-template <int kType, int kVecs, bool kEntropy>
-__device__ __forceinline__ void prob_grad_segment(const Segment<kType>& seg, float c,
-                                                  const ProbStats& st, const int64_t* targets,
-                                                  const ProbGrad<kType>& G) {
-    typename Elem<kType>::T* g = G.grad + seg.row * G.stride;
-    const int64_t t = targets ? targets[seg.row] : -1;
-    const bool given = t >= seg.first_id() && t < seg.end_id();
-    const bool in_row = t >= 0 && t < seg.vocab && st.on != 0.0f;
-    const float gl = in_row && G.grad_logprob ? G.grad_logprob[seg.row] * G.inv_t : 0.0f;
-    const float gh = kEntropy ? G.grad_entropy[seg.row] * G.inv_t : 0.0f;
-    const float A = -gl - gh * st.entropy, B = -gh * kLn2;
-    float at_t = 0.0f;
-    if (given && threadIdx.x == 0) {
-        const float d = (Elem<kType>::up(seg.x[t]) - st.m) * c - st.l2s;
-        at_t = exp2_hw(d) * (kEntropy ? __builtin_fmaf(B, fmaxf(d, -200.0f), A) : A) + gl;
+    template <bool kFast> __device__ __forceinline__ float value(float x) const {
+        const float d = h.exponent<kFast>(x);
+        return exp2_hw(d) * (kEntropy ? __builtin_fmaf(B, fmaxf(d, low), A) : A);
     }
-    __syncthreads();                             // read before a gradient that replaces it is written
-    const int n = seg.template chunks<kVecs>();
-    for (int ch = 0; ch < n; ++ch) prob_grad_chunk<kType, kVecs, kEntropy>(seg, ch, c, A, B, st, g);
-    __syncthreads();                             // after the dense pass's write of the same entry
-    if (given && threadIdx.x == 0) g[t] = Elem<kType>::down(at_t);
+    __device__ __forceinline__ float at_given(float x) const {
+        return (h.fast ? value<true>(x) : value<false>(x)) + gl;
+    }
+};
+template <int kType, bool kEntropy>
+__device__ __forceinline__ ProbCoef<kEntropy> prob_coef(const ProbStats& st, float c,
+                                                        const ProbGrad<kType>& G, int64_t row,
+                                                        bool given) {
+    const float gl = given && st.on != 0.0f && G.grad_logprob ? G.grad_logprob[row] * G.inv_t : 0.0f;
+    return ProbCoef<kEntropy>(st, c, gl, kEntropy ? G.grad_entropy[row] * G.inv_t : 0.0f);
 }
 
 template <int kType>
@@ -501,38 +436,23 @@ struct DistillGrad {
     float inv_t;
 };
 
-template <int kType, int kVecs>
-__device__ __forceinline__ void distill_grad_segment(const Segment<kType>& seg, float c,
-                                                     const DistillStats& st, const DistillIn& in,
-                                                     const DistillGrad<kType>& G) {
-    constexpr int E = Elem<kType>::kE;
-    typename Elem<kType>::T* g = G.grad + seg.row * G.stride;
-    const float w = st.on != 0.0f ? G.grad_loss[seg.row] * G.inv_t : 0.0f;
-    // wave 0 forms the listed entries' gradients before any gradient is written
-    int64_t id = -1;
-    float listed = 0.0f;
-    if (threadIdx.x < kWave) {
-        const int lane = threadIdx.x;
-        id = lane < in.top ? in.ids[seg.row * in.top + lane] : -1;
-        const bool ok = id >= 0 && id < seg.vocab;
-        const float nw = __builtin_rintf(st.norm);
-        float hi, lo;
-        const float q = ok ? teacher_q(in.tlp[seg.row * in.top + lane], nw, st.norm - nw, hi, lo) : 0.0f;
-        if (!ok) id = -1;
-        float sum = 0.0f;
-        for (int k = 0; k < in.top; ++k) {
-            const int other = __builtin_amdgcn_readlane((int)id, k);
-            const float oq = as_f32((uint32_t)__builtin_amdgcn_readlane((int)as_u32(q), k));
-            if (other == (int)id) sum += oq;
-        }
-        if (id < seg.first_id() || id >= seg.end_id()) id = -1;
-        if (id >= 0) {
-            const float p = exp2_hw((Elem<kType>::up(seg.x[id]) - st.m) * c - st.l2s);
-            listed = st.on != 0.0f ? w * (st.qr * p - sum) : 0.0f;
-        }
+// the unlisted entries' gradient a e_j
+struct RestCoef {
+    Shift h;
+    float a;
+    __device__ __forceinline__ RestCoef(const DistillStats& st, float c, float w)
+        : h(st.rest_m, c, st.rest_l2), a(w * st.coef) {
+        if (h.fast) a *= exp2_hw(-h.left);
     }
-    __syncthreads();
-    const float a = w * st.coef;
+    template <bool kFast> __device__ __forceinline__ float value(float x) const {
+        return a * exp2_hw(h.exponent<kFast>(x));
+    }
+};
+
+template <int kType, int kVecs, bool kFast, int kThreads, typename Coef>
+__device__ __forceinline__ void grad_words(const Segment<kType, kThreads>& seg, const Coef& k,
+                                           typename Elem<kType>::T* g) {
+    constexpr int E = Elem<kType>::kE;
     const int n = seg.template chunks<kVecs>();
     for (int ch = 0; ch < n; ++ch) {
         u32x4 r[kVecs];
@@ -541,16 +461,45 @@ __device__ __forceinline__ void distill_grad_segment(const Segment<kType>& seg, 
         for (int i = 0; i < kVecs; ++i) {
             float o[E];
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                o[e] = a * exp2_hw((Elem<kType>::get(r[i], e) - st.rest_m) * c - st.rest_l2);
+            for (int e = 0; e < E; ++e) o[e] = k.template value<kFast>(Elem<kType>::get(r[i], e));
             seg.template store<kVecs>(g, ch, i, pack<kType>(o));
         }
     }
-    __syncthreads();
-    if (id >= 0) g[id] = Elem<kType>::down(listed);
+}
+template <int kType, int kVecs, typename Coef>
+__device__ __forceinline__ void grad_segment(const Segment<kType>& seg, const Coef& k,
+                                             typename Elem<kType>::T* g) {
+    __syncthreads();             // the given or listed entries were read before they are replaced
+    if (k.h.fast) grad_words<kType, kVecs, true>(seg, k, g);
+    else grad_words<kType, kVecs, false>(seg, k, g);
+    __syncthreads();             // those entries' own gradients are written after the dense ones
 }
 
-// ---- kernels ------------------------------------------------------------------------
+template <int kType, int kVecs, bool kEntropy>
+__device__ __forceinline__ void prob_grad_segment(const Segment<kType>& seg, float c,
+                                                  const ProbStats& st, const Given& t,
+                                                  const ProbGrad<kType>& G) {
+    typename Elem<kType>::T* g = G.grad + seg.row * G.stride;
+    const auto k = prob_coef<kType, kEntropy>(st, c, G, seg.row, t.id >= 0);
+    grad_segment<kType, kVecs>(seg, k, g);
+    if (threadIdx.x == 0 && t.id >= seg.first_id() && t.id < seg.end_id())
+        g[t.id] = Elem<kType>::down(k.at_given(t.x));
+}
+
+template <int kType, int kVecs>
+__device__ __forceinline__ void distill_grad_segment(const Segment<kType>& seg, float c,
+                                                     const DistillStats& st, int top,
+                                                     const Listed& l, const DistillGrad<kType>& G) {
+    typename Elem<kType>::T* g = G.grad + seg.row * G.stride;
+    const float w = st.on != 0.0f ? G.grad_loss[seg.row] * G.inv_t : 0.0f;
+    grad_segment<kType, kVecs>(seg, RestCoef(st, c, w), g);
+    if (threadIdx.x < kWave) {
+        const float v = listed_grad(l, st, top, c, w);
+        if (l.id >= seg.first_id() && l.id < seg.end_id()) g[l.id] = Elem<kType>::down(v);
+    }
+}
+
+// ---- kernels: segments ------------------------------------------------------------------
 
 // Rows cut into nseg segments of `span` words each; one block per segment.
 template <int kType>
@@ -575,72 +524,54 @@ struct RowsIn {
     }
 };
 
+// Entries marked in a bitmap become -inf; `at` is the word's first entry there.
+template <int kType>
+__device__ __forceinline__ void leave_out(u32x4& r, const uint32_t* marks, int at) {
+    constexpr int E = Elem<kType>::kE;
+    const uint32_t bits = (marks[at >> 5] >> (at & 31)) & ((1u << E) - 1);
+    if (!bits) return;
+    constexpr uint32_t kInf = Elem<kType>::kMinusInf;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t mask;
+        if (kType == FLASHOPT_FP32) {
+            mask = 0u - (bits >> i & 1u);
+        } else {
+            mask = ((0u - (bits >> (2 * i) & 1u)) & 0xFFFFu) | ((0u - (bits >> (2 * i + 1) & 1u)) << 16);
+        }
+        r[i] = (r[i] & ~mask) | (kInf & mask);
+    }
+}
+
 // The part of a segment: each thread runs over its words with a maximum of its
 // own, rescaling what it has when a chunk raises it; the threads join at the
-// end.  Returned to every thread of wave 0.  kListed: `marks` has a bit set
-// for each entry to leave out.  kTop: the threads' largest entry of each chunk
-// goes to chunk_best, `mine` is its largest of all.
-template <int kType, int kVecs, bool kListed, bool kTop>
-__device__ __forceinline__ Part segment_part(const Segment<kType>& seg, float c,
+// end.  Every wave gets it.  kListed: `marks` has a bit set for each entry to
+// leave out.  kTop: the threads' largest entry of each chunk goes to
+// chunk_best, `mine` is its largest of all.
+template <int kType, int kVecs, bool kListed, bool kTop, int kThreads>
+__device__ __forceinline__ Part segment_part(const Segment<kType, kThreads>& seg, float c,
                                              const uint32_t* marks, float* chunk_best, Part* red,
                                              float& mine) {
-    constexpr int E = Elem<kType>::kE;
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int n = seg.template chunks<kVecs>();
-    float m = -INFINITY, s = 0.0f, u = 0.0f;
+    Sums<kType, !kListed, kTop> sums(c);
+    mine = -INFINITY;
     for (int ch = 0; ch < n; ++ch) {
         u32x4 r[kVecs];
         seg.template load<kVecs>(ch, r);
-        if (kListed) {
+        if (kListed)
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const int at = ((ch * kVecs + i) * kBlock + (int)threadIdx.x) * E;
-                const uint32_t bits = (marks[at >> 5] >> (at & 31)) & ((1u << E) - 1);
-                if (bits) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        if (bits >> e & 1) {
-                            if (kType == FLASHOPT_FP32) r[i][e & 3] = Elem<kType>::kMinusInf;
-                            else if (e & 1) r[i][e >> 1] = (r[i][e >> 1] & 0xFFFFu) | (Elem<kType>::kMinusInf & 0xFFFF0000u);
-                            else r[i][e >> 1] = (r[i][e >> 1] & 0xFFFF0000u) | (Elem<kType>::kMinusInf & 0xFFFFu);
-                        }
-                }
-            }
+            for (int i = 0; i < kVecs; ++i)
+                leave_out<kType>(r[i], marks, ((ch * kVecs + i) * kThreads + (int)threadIdx.x) * Elem<kType>::kE);
+        const float top = sums.template add<kVecs>(r);
+        if (kTop) {
+            chunk_best[ch * kThreads + threadIdx.x] = top;
+            mine = fmaxf(mine, top);
         }
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-            for (int e = 0; e < E; ++e) top = fmaxf(top, Elem<kType>::get(r[i], e));
-        if (kTop) chunk_best[ch * kBlock + threadIdx.x] = top;
-        const float m_new = fmaxf(m, top);
-        const float shift = m_new == -INFINITY ? 0.0f : m_new;    // nothing yet: every e_j is 0
-        const float D = fmaxf((m - m_new) * c, -200.0f), f = exp2_hw(D);
-        float cs = 0.0f, cu = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float d = (Elem<kType>::get(r[i], e) - shift) * c;
-                const float p = exp2_hw(d);
-                cs += p;
-                // p is 0 below -150: the bound keeps 0 * -inf out of the sum
-                if (!kListed) cu = __builtin_fmaf(p, fmaxf(d, -200.0f), cu);
-            }
-        if (!kListed) u = f * (u + D * s) + cu;
-        s = s * f + cs;
-        m = m_new;
     }
-    mine = m;
-    const float wm = wave_max(m);
-    const float D = fmaxf((m - wm) * c, -200.0f), f = exp2_hw(D);
-    // a lane of -inf alone has s = 0, one of NaN alone keeps it
-    const float ws = wave_sum(s * f), wu = kListed ? 0.0f : wave_sum(f * (u + D * s));
-    if (lane == 0) red[wave] = Part{wm, ws, wu, 0.0f};
+    const Part p = wave_part<!kListed>(sums.m, sums.s, sums.u, c);
+    if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave] = p;
     __syncthreads();
-    Part p = {-INFINITY, 0.0f, 0.0f, 0.0f};
-    if (wave == 0) p = join_parts(red, kWavesPerBlock, c);
-    return p;
+    return join_parts(red, kThreads / kWave, c);
 }
 
 template <int kType, int kVecs, bool kTop, int kGrad>            // kGrad 1: of logprob, 2: and of entropy
@@ -649,16 +580,14 @@ __global__ __launch_bounds__(kBlock) void prob_kernel(RowsIn<kType> in, ProbOut 
                                                       ProbGrad<kType> G) {
     extern __shared__ float chunk_best[];
     __shared__ Part red[kWavesPerBlock];
-    __shared__ ProbStats shared_stats;
     const Segment<kType> seg = in.segment(blockIdx.x);
     float mine;
     const Part p = segment_part<kType, kVecs, false, kTop>(seg, in.c, nullptr, chunk_best, red, mine);
+    const ProbStats st = prob_stats(p);
     if (in.nseg > 1) {
         if (threadIdx.x == 0) part[blockIdx.x] = p;
-    } else if (threadIdx.x == 0) {
-        const ProbStats st = prob_stats(p);
-        shared_stats = st;
-        write_prob<kType>(seg.x, seg.vocab, seg.row, in.c, st, out);
+    } else if (!kGrad && threadIdx.x == 0) {
+        write_prob(seg.row, in.c, st, given_token<kType>(seg.x, seg.vocab, seg.row, out.targets), out);
     }
     if (kTop) {
         __shared__ TopShared sh;
@@ -667,28 +596,80 @@ __global__ __launch_bounds__(kBlock) void prob_kernel(RowsIn<kType> in, ProbOut 
             segment_top<kType, kVecs>(seg, chunk_best, mine, top, sh, [&](uint32_t k, uint64_t e) { list[k] = e; });
         } else {
             segment_top<kType, kVecs>(seg, chunk_best, mine, top, sh, [&](uint32_t k, uint64_t e) {
-                write_top(out, seg.row, top, (int)k, e, in.c, shared_stats);
+                write_top(out, seg.row, top, (int)k, e, in.c, st);
             });
         }
     }
     if (kGrad) {
-        __syncthreads();
-        prob_grad_segment<kType, kVecs, kGrad == 2>(seg, in.c, shared_stats, out.targets, G);
+        const Given t = given_token<kType>(seg.x, seg.vocab, seg.row, out.targets);
+        if (threadIdx.x == 0) write_prob(seg.row, in.c, st, t, out);
+        prob_grad_segment<kType, kVecs, kGrad == 2>(seg, in.c, st, t, G);
     }
 }
 
+// The rows of several segments joined, one block a row.  The segments' lists
+// are candidates of the row's: their entries with the value's upper 16 bits
+// at or above the top-th largest of those, ranked against each other; if too
+// many are equal there, the lists are walked from their heads instead.
+constexpr int kJoinEntries = kMaxSegments * FLASHOPT_TOP_MAX / kBlock;       // per thread
+
 template <int kType>
-__global__ __launch_bounds__(kBlock) void prob_join_kernel(RowsIn<kType> in, int64_t rows,
-                                                           ProbOut out, int top, const Part* part,
+__global__ __launch_bounds__(kBlock) void prob_join_kernel(RowsIn<kType> in, ProbOut out, int top,
+                                                           const Part* part,
                                                            const uint64_t* lists) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int64_t row = (int64_t)blockIdx.x * kWavesPerBlock + threadIdx.x / kWave;
-    if (row >= rows) return;
+    __shared__ uint32_t count[2][kWavesPerBlock];
+    __shared__ uint64_t found[kBlock];
+    __shared__ uint32_t nfound;
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int64_t row = blockIdx.x;
+    const int total = in.nseg * top;
+    const uint64_t* list = lists + row * total;
+    uint64_t e[kJoinEntries];
+    if (top > 0)
+#pragma unroll
+        for (int i = 0; i < kJoinEntries; ++i) {
+            const int at = i * kBlock + threadIdx.x;
+            e[i] = at < total ? list[at] : 0;
+        }
     const ProbStats st = prob_stats(join_parts(part + row * in.nseg, in.nseg, in.c));
-    if (lane == 0) write_prob<kType>(in.logits + row * in.stride, in.vocab, row, in.c, st, out);
-    if (top > 0) {
+    if (threadIdx.x == 0) {
+        nfound = 0;
+        const typename Elem<kType>::T* x = in.logits + row * in.stride;
+        write_prob(row, in.c, st, given_token<kType>(x, in.vocab, row, out.targets), out);
+    }
+    if (top == 0) return;
+    uint32_t bound = 0;
+    for (int bit = 15; bit >= 0; --bit) {
+        const uint32_t trial = bound | (1u << bit);
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 0; i < kJoinEntries; ++i)
+            if (i * kBlock < total) n += __popcll(__ballot((uint32_t)(e[i] >> 48) >= trial));
+        if (lane == 0) count[bit & 1][wave] = n;
+        __syncthreads();
+        n = 0;
+#pragma unroll
+        for (int w = 0; w < kWavesPerBlock; ++w) n += count[bit & 1][w];
+        if (n >= (uint32_t)top) bound = trial;
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinEntries; ++i)
+        if (i * kBlock < total && e[i] != 0 && (uint32_t)(e[i] >> 48) >= bound) {
+            const uint32_t at = atomicAdd(&nfound, 1u);
+            if (at < (uint32_t)kBlock) found[at] = e[i];
+        }
+    __syncthreads();
+    const uint32_t n = nfound;
+    if (n <= (uint32_t)kBlock) {
+        if (threadIdx.x < n) {
+            const uint64_t x = found[threadIdx.x];
+            uint32_t rank = 0;
+            for (uint32_t j = 0; j < n; ++j) rank += found[j] > x ? 1u : 0u;
+            if (rank < (uint32_t)top) write_top(out, row, top, (int)rank, x, in.c, st);
+        }
+    } else if (wave == 0) {
         // lane b walks the list of segment b, best first (a row has at most 64)
-        const uint64_t* mine = lists + (row * in.nseg + lane) * top;
+        const uint64_t* mine = list + (int64_t)lane * top;
         int at = 0;
         uint64_t head = lane < in.nseg ? mine[0] : 0;
         for (int k = 0; k < top; ++k) {
@@ -699,12 +680,31 @@ __global__ __launch_bounds__(kBlock) void prob_join_kernel(RowsIn<kType> in, int
     }
 }
 
+// The gradient from stats (the backward call), or, with `part`, from the
+// segments' parts of the same call, which the row's first block also writes
+// out.
 template <int kType, int kVecs, bool kEntropy>
-__global__ __launch_bounds__(kBlock) void prob_grad_kernel(RowsIn<kType> in, const int64_t* targets,
+__global__ __launch_bounds__(kBlock) void prob_grad_kernel(RowsIn<kType> in, ProbOut out,
+                                                           const Part* part,
                                                            const ProbStats* stats,
                                                            ProbGrad<kType> G) {
     const Segment<kType> seg = in.segment(blockIdx.x);
-    prob_grad_segment<kType, kVecs, kEntropy>(seg, in.c, stats[seg.row], targets, G);
+    const Given t = given_token<kType>(seg.x, seg.vocab, seg.row, out.targets);
+    const ProbStats st = part ? prob_stats(join_parts(part + seg.row * in.nseg, in.nseg, in.c))
+                              : stats[seg.row];
+    if (part && seg.begin == 0 && threadIdx.x == 0) write_prob(seg.row, in.c, st, t, out);
+    prob_grad_segment<kType, kVecs, kEntropy>(seg, in.c, st, t, G);
+}
+
+// The list of a row as wave 0 holds it; the row's numbers of it for all.
+template <int kType>
+__device__ __forceinline__ void share_list(const Segment<kType>& seg, float c, const DistillIn& list,
+                                           Listed& l, ListRow& shared) {
+    l.id = -1;
+    if (threadIdx.x < kWave) {
+        const ListRow lr = list_row<kType>(seg.x, seg.vocab, seg.row, c, list, l);
+        if (threadIdx.x == 0) shared = lr;
+    }
 }
 
 template <int kType, int kVecs, bool kGrad>
@@ -714,7 +714,7 @@ __global__ __launch_bounds__(kBlock) void distill_kernel(RowsIn<kType> in, Disti
                                                          DistillGrad<kType> G) {
     extern __shared__ uint32_t marks[];
     __shared__ Part red[kWavesPerBlock];
-    __shared__ DistillStats shared_stats;
+    __shared__ ListRow lr;
     const Segment<kType> seg = in.segment(blockIdx.x);
     const int words = seg.template chunks<kVecs>() * (kChunk<kType, kVecs> / 32);
     for (int i = threadIdx.x; i < words; i += kBlock) marks[i] = 0;
@@ -724,48 +724,56 @@ __global__ __launch_bounds__(kBlock) void distill_kernel(RowsIn<kType> in, Disti
         const int64_t at = id - seg.first_id();
         if (id >= seg.first_id() && id < seg.end_id()) atomicOr(&marks[at >> 5], 1u << (at & 31));
     }
+    Listed l;
+    l.id = -1;
+    if (in.nseg == 1) share_list<kType>(seg, in.c, list, l, lr);
     __syncthreads();
     float mine;
     const Part p = segment_part<kType, kVecs, true, false>(seg, in.c, marks, nullptr, red, mine);
     if (in.nseg > 1) {
         if (threadIdx.x == 0) part[blockIdx.x] = p;
-    } else if (threadIdx.x < kWave) {
-        float l;
-        const DistillStats st = distill_stats<kType>(seg.x, seg.vocab, seg.row, in.c, in.c_low, list, p, l);
-        if (threadIdx.x == 0) {
-            if (loss) loss[seg.row] = l;
-            stats[seg.row] = st;
-            shared_stats = st;
-        }
+        return;
     }
-    if (kGrad) {
-        __syncthreads();
-        distill_grad_segment<kType, kVecs>(seg, in.c, shared_stats, list, G);
-    }
+    const DistillStats st = finish_row(p, lr, list.tail, in.c, in.c_low, l, seg.row, loss, stats, true);
+    if (kGrad) distill_grad_segment<kType, kVecs>(seg, in.c, st, list.top, l, G);
 }
 
+// one wave a row
 template <int kType>
-__global__ __launch_bounds__(kBlock) void distill_join_kernel(RowsIn<kType> in, int64_t rows,
-                                                              DistillIn list, const Part* part,
-                                                              float* loss, DistillStats* stats) {
-    const int64_t row = (int64_t)blockIdx.x * kWavesPerBlock + threadIdx.x / kWave;
-    if (row >= rows) return;
-    const Part rest = join_parts(part + row * in.nseg, in.nseg, in.c);
-    float l;
-    const DistillStats st = distill_stats<kType>(in.logits + row * in.stride, in.vocab, row, in.c,
-                                                 in.c_low, list, rest, l);
-    if ((threadIdx.x & (kWave - 1)) == 0) {
-        if (loss) loss[row] = l;
-        stats[row] = st;
-    }
+__global__ __launch_bounds__(kWave) void distill_join_kernel(RowsIn<kType> in, DistillIn list,
+                                                             const Part* part, float* loss,
+                                                             DistillStats* stats) {
+    const int64_t row = blockIdx.x;
+    Listed l;
+    const ListRow lr = list_row<kType>(in.logits + row * in.stride, in.vocab, row, in.c, list, l);
+    finish_row(join_parts(part + row * in.nseg, in.nseg, in.c), lr, list.tail, in.c, in.c_low, l,
+               row, loss, stats, true);
 }
 
+// As prob_grad_kernel.
 template <int kType, int kVecs>
 __global__ __launch_bounds__(kBlock) void distill_grad_kernel(RowsIn<kType> in, DistillIn list,
+                                                              const Part* part, float* loss,
                                                               const DistillStats* stats,
                                                               DistillGrad<kType> G) {
+    __shared__ ListRow lr;
     const Segment<kType> seg = in.segment(blockIdx.x);
-    distill_grad_segment<kType, kVecs>(seg, in.c, stats[seg.row], list, G);
+    Listed l;
+    DistillStats st;
+    if (part) {
+        share_list<kType>(seg, in.c, list, l, lr);
+        __syncthreads();
+        st = finish_row(join_parts(part + seg.row * in.nseg, in.nseg, in.c), lr, list.tail, in.c,
+                        in.c_low, l, seg.row, loss, nullptr, seg.begin == 0);
+    } else {
+        st = stats[seg.row];
+        share_list<kType>(seg, in.c, list, l, lr);
+        if (threadIdx.x < kWave && l.id >= 0) {  // q by the forward call's norm
+            const float n = __builtin_rintf(st.norm);
+            l.q = list_q(l, n, st.norm - n, l.q);
+        }
+    }
+    distill_grad_segment<kType, kVecs>(seg, in.c, st, list.top, l, G);
 }
 
 // ---- host ---------------------------------------------------------------------
@@ -811,7 +819,6 @@ static int check_list(const int64_t* top_id, const float* top_logprob, int32_t t
 // which one wave joins), and with very few the chunks are the short ones.  A
 // segment is at most kMaxChunks chunks, whose maxima or marks lie in LDS.
 constexpr int64_t kBlocksWanted = 1024;
-constexpr int64_t kMaxSegments = 64;
 constexpr int kMaxChunks = 16;
 struct Cut {
     int vecs;
@@ -854,13 +861,6 @@ static int by_type(int32_t type, int vecs, F f) {
     return launch_status();
 }
 
-struct Rows {                                    // a call's logits
-    const void* logits;
-    int32_t type;
-    int64_t rows, vocab, stride;
-    double temperature;
-};
-
 template <int kType>
 static RowsIn<kType> rows_in(const Rows& a, const Cut& k) {
     RowsIn<kType> in;
@@ -875,15 +875,35 @@ static RowsIn<kType> rows_in(const Rows& a, const Cut& k) {
     return in;
 }
 
-static dim3 join_grid(int64_t rows) {
-    return dim3((unsigned)((rows + kWavesPerBlock - 1) / kWavesPerBlock));
+template <int kType>
+static ProbGrad<kType> prob_grad(const Rows& a, const Upstream& g) {
+    return {g.logprob, g.entropy, (typename Elem<kType>::T*)g.grad, g.stride,
+            (float)(1.0 / a.temperature)};
+}
+template <int kType>
+static DistillGrad<kType> distill_grad(const Rows& a, const Upstream& g) {
+    return {g.logprob, (typename Elem<kType>::T*)g.grad, g.stride, (float)(1.0 / a.temperature)};
 }
 
-// The forward pass; with `grad`, rows that one block holds get their gradient
-// in the same launch, others in one more.
+// The gradient of cut rows: from stats, or from the parts of the same call.
+static int launch_prob_grad(const Rows& a, const Cut& k, const ProbOut& out, const Part* part,
+                            const float* stats, const Upstream& g, hipStream_t st) {
+    return by_type(a.type, k.vecs, [&](auto t, auto v) {
+        constexpr int kType = decltype(t)::value, kVecs = decltype(v)::value;
+        const dim3 grid((unsigned)(a.rows * k.nseg));
+        if (g.entropy)
+            hipLaunchKernelGGL((prob_grad_kernel<kType, kVecs, true>), grid, dim3(kBlock), 0, st,
+                               rows_in<kType>(a, k), out, part, (const ProbStats*)stats,
+                               prob_grad<kType>(a, g));
+        else
+            hipLaunchKernelGGL((prob_grad_kernel<kType, kVecs, false>), grid, dim3(kBlock), 0, st,
+                               rows_in<kType>(a, k), out, part, (const ProbStats*)stats,
+                               prob_grad<kType>(a, g));
+    });
+}
+
 static int launch_prob(const Rows& a, const ProbOut& out, int32_t top, void* workspace,
-                       const float* grad_logprob, const float* grad_entropy, void* grad,
-                       int64_t grad_stride, hipStream_t st) {
+                       hipStream_t st) {
     const Cut k = cut_rows(a.type, a.rows, a.vocab);
     Part* part = (Part*)workspace;
     uint64_t* lists = (uint64_t*)((char*)workspace + parts_bytes(k, a.rows));
@@ -891,86 +911,79 @@ static int launch_prob(const Rows& a, const ProbOut& out, int32_t top, void* wor
         constexpr int kType = decltype(t)::value, kVecs = decltype(v)::value;
         const RowsIn<kType> in = rows_in<kType>(a, k);
         const dim3 grid((unsigned)(a.rows * k.nseg));
-        const ProbGrad<kType> G = {grad_logprob, grad_entropy, (typename Elem<kType>::T*)grad,
-                                   grad_stride, (float)(1.0 / a.temperature)};
-        const size_t lds = top > 0 ? (size_t)k.chunks * kBlock * sizeof(float) : 0;
+        const ProbGrad<kType> none = {};
         if (top > 0)
-            hipLaunchKernelGGL((prob_kernel<kType, kVecs, true, 0>), grid, dim3(kBlock), lds, st, in,
-                               out, top, part, lists, G);
-        else if (!grad || k.nseg > 1)
+            hipLaunchKernelGGL((prob_kernel<kType, kVecs, true, 0>), grid, dim3(kBlock),
+                               (size_t)k.chunks * kBlock * sizeof(float), st, in, out, top, part,
+                               lists, none);
+        else
             hipLaunchKernelGGL((prob_kernel<kType, kVecs, false, 0>), grid, dim3(kBlock), 0, st, in,
-                               out, 0, part, lists, G);
-        else if (grad_entropy)
-            hipLaunchKernelGGL((prob_kernel<kType, kVecs, false, 2>), grid, dim3(kBlock), 0, st, in,
-                               out, 0, part, lists, G);
-        else
-            hipLaunchKernelGGL((prob_kernel<kType, kVecs, false, 1>), grid, dim3(kBlock), 0, st, in,
-                               out, 0, part, lists, G);
+                               out, 0, part, lists, none);
         if (k.nseg > 1)
-            hipLaunchKernelGGL((prob_join_kernel<kType>), join_grid(a.rows), dim3(kBlock), 0, st, in,
-                               a.rows, out, top, part, lists);
+            hipLaunchKernelGGL((prob_join_kernel<kType>), dim3((unsigned)a.rows), dim3(kBlock), 0,
+                               st, in, out, top, part, lists);
     });
 }
 
-static int launch_prob_grad(const Rows& a, const int64_t* targets, const float* stats,
-                            const float* grad_logprob, const float* grad_entropy, void* grad,
-                            int64_t grad_stride, hipStream_t st) {
-    Cut k = cut_rows(a.type, a.rows, a.vocab);
-    return by_type(a.type, k.vecs, [&](auto t, auto v) {
-        constexpr int kType = decltype(t)::value, kVecs = decltype(v)::value;
-        const RowsIn<kType> in = rows_in<kType>(a, k);
-        const dim3 grid((unsigned)(a.rows * k.nseg));
-        const ProbGrad<kType> G = {grad_logprob, grad_entropy, (typename Elem<kType>::T*)grad,
-                                   grad_stride, (float)(1.0 / a.temperature)};
-        if (grad_entropy)
-            hipLaunchKernelGGL((prob_grad_kernel<kType, kVecs, true>), grid, dim3(kBlock), 0, st, in,
-                               targets, (const ProbStats*)stats, G);
-        else
-            hipLaunchKernelGGL((prob_grad_kernel<kType, kVecs, false>), grid, dim3(kBlock), 0, st, in,
-                               targets, (const ProbStats*)stats, G);
-    });
-}
-
-static int launch_distill(const Rows& a, const DistillIn& list, void* workspace, float* loss,
-                          float* stats, const float* grad_loss, void* grad, int64_t grad_stride,
-                          hipStream_t st) {
+static int launch_prob_both(const Rows& a, const ProbOut& out, void* workspace, const Upstream& g,
+                            hipStream_t st) {
+    if (launch_rows_prob(a, out, g, st)) return launch_status();
     const Cut k = cut_rows(a.type, a.rows, a.vocab);
     Part* part = (Part*)workspace;
-    return by_type(a.type, k.vecs, [&](auto t, auto v) {
+    const int f = by_type(a.type, k.vecs, [&](auto t, auto v) {
         constexpr int kType = decltype(t)::value, kVecs = decltype(v)::value;
         const RowsIn<kType> in = rows_in<kType>(a, k);
         const dim3 grid((unsigned)(a.rows * k.nseg));
-        const DistillGrad<kType> G = {grad_loss, (typename Elem<kType>::T*)grad, grad_stride,
-                                      (float)(1.0 / a.temperature)};
+        const ProbGrad<kType> G = prob_grad<kType>(a, g);
+        if (k.nseg > 1)
+            hipLaunchKernelGGL((prob_kernel<kType, kVecs, false, 0>), grid, dim3(kBlock), 0, st, in,
+                               out, 0, part, nullptr, G);
+        else if (g.entropy)
+            hipLaunchKernelGGL((prob_kernel<kType, kVecs, false, 2>), grid, dim3(kBlock), 0, st, in,
+                               out, 0, part, nullptr, G);
+        else
+            hipLaunchKernelGGL((prob_kernel<kType, kVecs, false, 1>), grid, dim3(kBlock), 0, st, in,
+                               out, 0, part, nullptr, G);
+    });
+    if (f || k.nseg == 1) return f;
+    return launch_prob_grad(a, k, out, part, nullptr, g, st);
+}
+
+static int launch_distill_grad(const Rows& a, const Cut& k, const DistillIn& list,
+                               const Part* part, float* loss, const float* stats,
+                               const Upstream& g, hipStream_t st) {
+    return by_type(a.type, k.vecs, [&](auto t, auto v) {
+        constexpr int kType = decltype(t)::value, kVecs = decltype(v)::value;
+        hipLaunchKernelGGL((distill_grad_kernel<kType, kVecs>), dim3((unsigned)(a.rows * k.nseg)),
+                           dim3(kBlock), 0, st, rows_in<kType>(a, k), list, part, loss,
+                           (const DistillStats*)stats, distill_grad<kType>(a, g));
+    });
+}
+
+// grad null: the forward pass alone
+static int launch_distill(const Rows& a, const DistillIn& list, void* workspace, float* loss,
+                          float* stats, const Upstream& g, hipStream_t st) {
+    const Cut k = cut_rows(a.type, a.rows, a.vocab);
+    if (g.grad && launch_rows_distill(a, list, loss, g, st)) return launch_status();
+    Part* part = (Part*)workspace;
+    const int f = by_type(a.type, k.vecs, [&](auto t, auto v) {
+        constexpr int kType = decltype(t)::value, kVecs = decltype(v)::value;
+        const RowsIn<kType> in = rows_in<kType>(a, k);
+        const dim3 grid((unsigned)(a.rows * k.nseg));
+        const DistillGrad<kType> G = distill_grad<kType>(a, g);
         const size_t lds = (size_t)k.chunks * kChunk<kType, kVecs> / 8;
-        if (grad && k.nseg == 1)
+        if (g.grad && k.nseg == 1)
             hipLaunchKernelGGL((distill_kernel<kType, kVecs, true>), grid, dim3(kBlock), lds, st, in,
                                list, part, loss, (DistillStats*)stats, G);
         else
             hipLaunchKernelGGL((distill_kernel<kType, kVecs, false>), grid, dim3(kBlock), lds, st, in,
                                list, part, loss, (DistillStats*)stats, G);
-        if (k.nseg > 1) {
-            hipLaunchKernelGGL((distill_join_kernel<kType>), join_grid(a.rows), dim3(kBlock), 0, st,
-                               in, a.rows, list, part, loss, (DistillStats*)stats);
-            if (grad)
-                hipLaunchKernelGGL((distill_grad_kernel<kType, kVecs>), grid, dim3(kBlock), 0, st, in,
-                                   list, (const DistillStats*)stats, G);
-        }
+        if (k.nseg > 1 && !g.grad)
+            hipLaunchKernelGGL((distill_join_kernel<kType>), dim3((unsigned)a.rows), dim3(kWave), 0,
+                               st, in, list, part, loss, (DistillStats*)stats);
     });
-}
-
-static int launch_distill_grad(const Rows& a, const DistillIn& list, const float* stats,
-                               const float* grad_loss, void* grad, int64_t grad_stride,
-                               hipStream_t st) {
-    const Cut k = cut_rows(a.type, a.rows, a.vocab);
-    return by_type(a.type, k.vecs, [&](auto t, auto v) {
-        constexpr int kType = decltype(t)::value, kVecs = decltype(v)::value;
-        const DistillGrad<kType> G = {grad_loss, (typename Elem<kType>::T*)grad, grad_stride,
-                                      (float)(1.0 / a.temperature)};
-        hipLaunchKernelGGL((distill_grad_kernel<kType, kVecs>), dim3((unsigned)(a.rows * k.nseg)),
-                           dim3(kBlock), 0, st, rows_in<kType>(a, k), list,
-                           (const DistillStats*)stats, G);
-    });
+    if (f || k.nseg == 1 || !g.grad) return f;
+    return launch_distill_grad(a, k, list, part, loss, nullptr, g, st);
 }
 
 }  // namespace flashopt
@@ -1005,7 +1018,7 @@ int flashopt_logprob(const void* logits, int32_t type, int64_t rows, int64_t voc
     if (w) return w;
     return launch_prob({logits, type, rows, vocab, stride, temperature},
                        {targets, logprob, entropy, (ProbStats*)stats, top_logprob, top_id}, top,
-                       workspace, nullptr, nullptr, nullptr, 0, (hipStream_t)stream);
+                       workspace, (hipStream_t)stream);
 }
 
 int flashopt_logprob_backward(const void* logits, int32_t type, int64_t rows, int64_t vocab,
@@ -1022,34 +1035,32 @@ int flashopt_logprob_backward(const void* logits, int32_t type, int64_t rows, in
         return FLASHOPT_ERR_ALIGN;
     const int g = check_grad(grad, type, vocab, grad_stride);
     if (g) return g;
-    return launch_prob_grad({logits, type, rows, vocab, stride, temperature}, targets, stats,
-                            grad_logprob, grad_entropy, grad, grad_stride, (hipStream_t)stream);
+    return launch_prob_grad({logits, type, rows, vocab, stride, temperature},
+                            cut_rows(type, rows, vocab),
+                            {targets, nullptr, nullptr, nullptr, nullptr, nullptr}, nullptr, stats,
+                            {grad_logprob, grad_entropy, grad, grad_stride}, (hipStream_t)stream);
 }
 
 int flashopt_logprob_grad(const void* logits, int32_t type, int64_t rows, int64_t vocab,
                           int64_t stride, double temperature, const int64_t* targets,
                           const float* grad_logprob, const float* grad_entropy, void* workspace,
-                          size_t workspace_bytes, float* logprob, float* entropy, float* stats,
-                          void* grad, int64_t grad_stride, void* stream) {
+                          size_t workspace_bytes, float* logprob, float* entropy, void* grad,
+                          int64_t grad_stride, void* stream) {
     const int e = check_rows(logits, type, rows, vocab, stride, temperature);
     if (e) return e;
     if (rows == 0) return FLASHOPT_OK;
-    if (!stats || ((logprob || grad_logprob) && !targets)) return FLASHOPT_ERR_NULL;
+    if ((logprob || grad_logprob) && !targets) return FLASHOPT_ERR_NULL;
     if (!aligned(targets, 8) || !aligned(logprob, 4) || !aligned(entropy, 4) ||
-        !aligned(stats, 16) || !aligned(grad_logprob, 4) || !aligned(grad_entropy, 4))
+        !aligned(grad_logprob, 4) || !aligned(grad_entropy, 4))
         return FLASHOPT_ERR_ALIGN;
     const int g = check_grad(grad, type, vocab, grad_stride);
     if (g) return g;
     const int w = check_workspace(workspace, workspace_bytes,
                                   flashopt_logprob_workspace_bytes(type, rows, vocab, 0));
     if (w) return w;
-    const Rows a = {logits, type, rows, vocab, stride, temperature};
-    const int f = launch_prob(a, {targets, logprob, entropy, (ProbStats*)stats, nullptr, nullptr}, 0,
-                              workspace, grad_logprob, grad_entropy, grad, grad_stride,
-                              (hipStream_t)stream);
-    if (f || cut_rows(type, rows, vocab).nseg == 1) return f;
-    return launch_prob_grad(a, targets, stats, grad_logprob, grad_entropy, grad, grad_stride,
-                            (hipStream_t)stream);
+    return launch_prob_both({logits, type, rows, vocab, stride, temperature},
+                            {targets, logprob, entropy, nullptr, nullptr, nullptr}, workspace,
+                            {grad_logprob, grad_entropy, grad, grad_stride}, (hipStream_t)stream);
 }
 
 size_t flashopt_distill_workspace_bytes(int32_t type, int64_t rows, int64_t vocab) {
@@ -1073,8 +1084,8 @@ int flashopt_distill(const void* logits, int32_t type, int64_t rows, int64_t voc
                                   flashopt_distill_workspace_bytes(type, rows, vocab));
     if (w) return w;
     return launch_distill({logits, type, rows, vocab, stride, temperature},
-                          {top_id, top_logprob, top, tail}, workspace, loss, stats, nullptr, nullptr,
-                          0, (hipStream_t)stream);
+                          {top_id, top_logprob, top, tail}, workspace, loss, stats, {},
+                          (hipStream_t)stream);
 }
 
 int flashopt_distill_backward(const void* logits, int32_t type, int64_t rows, int64_t vocab,
@@ -1093,7 +1104,8 @@ int flashopt_distill_backward(const void* logits, int32_t type, int64_t rows, in
     const int g = check_grad(grad, type, vocab, grad_stride);
     if (g) return g;
     return launch_distill_grad({logits, type, rows, vocab, stride, temperature},
-                               {top_id, top_logprob, top, 0}, stats, grad_loss, grad, grad_stride,
+                               cut_rows(type, rows, vocab), {top_id, top_logprob, top, 1}, nullptr,
+                               nullptr, stats, {grad_loss, nullptr, grad, grad_stride},
                                (hipStream_t)stream);
 }
 
@@ -1101,7 +1113,7 @@ int flashopt_distill_grad(const void* logits, int32_t type, int64_t rows, int64_
                           int64_t stride, double temperature, const int64_t* top_id,
                           const float* top_logprob, int32_t top, int32_t tail,
                           const float* grad_loss, void* workspace, size_t workspace_bytes,
-                          float* loss, float* stats, void* grad, int64_t grad_stride,
+                          float* loss, void* grad, int64_t grad_stride,
                           void* stream) {
     const int e = check_rows(logits, type, rows, vocab, stride, temperature);
     if (e) return e;
@@ -1110,17 +1122,16 @@ int flashopt_distill_grad(const void* logits, int32_t type, int64_t rows, int64_
     if (rows == 0) return FLASHOPT_OK;
     const int l = check_list(top_id, top_logprob, top, vocab);
     if (l) return l;
-    if (!stats || !grad_loss) return FLASHOPT_ERR_NULL;
-    if (!aligned(stats, 16) || !aligned(loss, 4) || !aligned(grad_loss, 4))
-        return FLASHOPT_ERR_ALIGN;
+    if (!grad_loss) return FLASHOPT_ERR_NULL;
+    if (!aligned(loss, 4) || !aligned(grad_loss, 4)) return FLASHOPT_ERR_ALIGN;
     const int g = check_grad(grad, type, vocab, grad_stride);
     if (g) return g;
     const int w = check_workspace(workspace, workspace_bytes,
                                   flashopt_distill_workspace_bytes(type, rows, vocab));
     if (w) return w;
     return launch_distill({logits, type, rows, vocab, stride, temperature},
-                          {top_id, top_logprob, top, tail}, workspace, loss, stats, grad_loss, grad,
-                          grad_stride, (hipStream_t)stream);
+                          {top_id, top_logprob, top, tail}, workspace, loss, nullptr,
+                          {grad_loss, nullptr, grad, grad_stride}, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -148,14 +148,14 @@ SIGNATURES = {
     "flashopt_logprob_backward": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _D, _P, _P, _P, _P,
                                                  _P, _I64, _P]),
     "flashopt_logprob_grad": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _D, _P, _P, _P, _P, _SZ,
-                                             _P, _P, _P, _P, _I64, _P]),
+                                             _P, _P, _P, _I64, _P]),
     "flashopt_distill_workspace_bytes": (_SZ, [_I32, _I64, _I64]),
     "flashopt_distill": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _D, _P, _P, _I32, _I32, _P,
                                         _SZ, _P, _P, _P]),
     "flashopt_distill_backward": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _D, _P, _P, _I32, _P,
                                                  _P, _P, _I64, _P]),
     "flashopt_distill_grad": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _D, _P, _P, _I32, _I32,
-                                             _P, _P, _SZ, _P, _P, _P, _I64, _P]),
+                                             _P, _P, _SZ, _P, _P, _I64, _P]),
     "flashopt_int8_ld": (_I64, [_I64]),
     "flashopt_quantize_rows": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _P, _P, _P]),
     "flashopt_tensor_quantize_rows": (ctypes.c_int, [ctypes.POINTER(Tensor), _I32, _I64, _P, _P,
@@ -852,7 +852,7 @@ def flashopt_logprob_backward(logits, targets, stats, grad_logprob, grad_entropy
           _arg(grad_entropy, torch.float32, rows, dev, "grad_entropy"), g, gs)
 
 
-def flashopt_logprob_grad(logits, targets, grad_logprob, grad_entropy, stats, grad, logprob=None,
+def flashopt_logprob_grad(logits, targets, grad_logprob, grad_entropy, grad, logprob=None,
                           entropy=None, temperature: float = 1.0, workspace=None,
                           stream=None) -> None:
     x, ty, rows, vocab, stride = _logits(logits)
@@ -865,8 +865,7 @@ def flashopt_logprob_grad(logits, targets, grad_logprob, grad_entropy, stats, gr
           _arg(grad_logprob, torch.float32, rows, dev, "grad_logprob"),
           _arg(grad_entropy, torch.float32, rows, dev, "grad_entropy"), wp, wb,
           _arg(logprob, torch.float32, rows, dev, "logprob"),
-          _arg(entropy, torch.float32, rows, dev, "entropy"),
-          _arg(stats, torch.float32, 4 * rows, dev, "stats"), g, gs)
+          _arg(entropy, torch.float32, rows, dev, "entropy"), g, gs)
 
 
 def _listed(top_id, top_logprob, rows: int, dev):
@@ -900,7 +899,7 @@ def flashopt_distill_backward(logits, top_id, top_logprob, stats, grad_loss, gra
           _arg(grad_loss, torch.float32, rows, dev, "grad_loss"), g, gs)
 
 
-def flashopt_distill_grad(logits, top_id, top_logprob, grad_loss, loss, stats, grad,
+def flashopt_distill_grad(logits, top_id, top_logprob, grad_loss, loss, grad,
                           tail: bool = True, temperature: float = 1.0, workspace=None,
                           stream=None) -> None:
     x, ty, rows, vocab, stride = _logits(logits)
@@ -911,8 +910,7 @@ def flashopt_distill_grad(logits, top_id, top_logprob, grad_loss, loss, stats, g
     wp, wb, _ws = _scratch(workspace, need, dev, stream)
     _call("flashopt_distill_grad", dev, stream, x, ty, rows, vocab, stride, temperature, ids, tlp,
           top, int(tail), _arg(grad_loss, torch.float32, rows, dev, "grad_loss"), wp, wb,
-          _arg(loss, torch.float32, rows, dev, "loss"),
-          _arg(stats, torch.float32, 8 * rows, dev, "stats"), g, gs)
+          _arg(loss, torch.float32, rows, dev, "loss"), g, gs)
 
 
 def flashopt_quantize_rows(x, codes, scale, stream=None) -> None:

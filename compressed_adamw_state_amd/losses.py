@@ -176,13 +176,13 @@ def token_logprobs_grad(logits: torch.Tensor, targets: torch.Tensor, grad_logpro
     if grad_entropy is not None:
         grad_entropy = _per_row(grad_entropy, lead, dev, torch.float32, "grad_entropy")
     x, ty, rows, vocab, stride = F._logits(_rows(logits))
-    logprob, entropy, stats = _empty(lead, dev), _empty(lead, dev), _empty((rows, 4), dev)
+    logprob, entropy = _empty(lead, dev), _empty(lead, dev)
     grad, grad_stride = _grad_buffer(logits, inplace)
     need = F.lib().flashopt_logprob_workspace_bytes(ty, rows, vocab, 0)
     ws = _workspace(need, dev)
     F._call("flashopt_logprob_grad", dev, None, x, ty, rows, vocab, stride, temperature,
             targets.data_ptr(), grad_logprob.data_ptr(), _at(grad_entropy), _at(ws), need,
-            logprob.data_ptr(), entropy.data_ptr(), stats.data_ptr(), grad.data_ptr(), grad_stride)
+            logprob.data_ptr(), entropy.data_ptr(), grad.data_ptr(), grad_stride)
     return TokenLogprobsGrad(logprob, entropy, grad)
 
 
@@ -257,12 +257,11 @@ def distill_grad(logits: torch.Tensor, top_id: torch.Tensor, top_logprob: torch.
     top_id, top_logprob = _teacher(logits, lead, top_id, top_logprob)
     grad_loss = _per_row(grad_loss, lead, dev, torch.float32, "grad_loss")
     x, ty, rows, vocab, stride = F._logits(_rows(logits))
-    loss, stats = _empty(lead, dev), _empty((rows, 8), dev)
+    loss = _empty(lead, dev)
     grad, grad_stride = _grad_buffer(logits, inplace)
     need = F.lib().flashopt_distill_workspace_bytes(ty, rows, vocab)
     ws = _workspace(need, dev)
     F._call("flashopt_distill_grad", dev, None, x, ty, rows, vocab, stride, temperature,
             top_id.data_ptr(), top_logprob.data_ptr(), top_id.shape[-1], bool(tail),
-            grad_loss.data_ptr(), _at(ws), need, loss.data_ptr(), stats.data_ptr(),
-            grad.data_ptr(), grad_stride)
+            grad_loss.data_ptr(), _at(ws), need, loss.data_ptr(), grad.data_ptr(), grad_stride)
     return loss, grad

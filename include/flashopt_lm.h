@@ -53,7 +53,9 @@ typedef enum flashopt_type {
 #define FLASHOPT_VOCAB_MAX 524288
 #define FLASHOPT_TOP_MAX 64
 
-/* Per row: the log probability of targets[r], the entropy
+/* The workspace sizes may be 0 (NULL will do then).
+ *
+ * Per row: the log probability of targets[r], the entropy
  * -sum_j p_j log p_j, the `top` largest entries (their log probabilities and
  * ids, largest first, equal logits by lowest id), and `stats`, four binary32
  * numbers that the backward call reads.  targets may be NULL (logprob then
@@ -80,8 +82,8 @@ int flashopt_logprob_backward(const void* logits, int32_t type, int64_t rows, in
 int flashopt_logprob_grad(const void* logits, int32_t type, int64_t rows, int64_t vocab,
                           int64_t stride, double temperature, const int64_t* targets,
                           const float* grad_logprob, const float* grad_entropy, void* workspace,
-                          size_t workspace_bytes, float* logprob, float* entropy, float* stats,
-                          void* grad, int64_t grad_stride, void* stream);
+                          size_t workspace_bytes, float* logprob, float* entropy, void* grad,
+                          int64_t grad_stride, void* stream);
 
 /* Distillation.  A teacher gives each row `top` token ids and their log
  * probabilities t_k at the same temperature (flashopt_logprob's top_id and
@@ -95,7 +97,8 @@ int flashopt_logprob_grad(const void* logits, int32_t type, int64_t rows, int64_
  * Q = sum_k q_k the gradient with respect to the logits is
  *   grad_j = (g/T) (p_j (Q + r) - sum_{k: id_k = j} q_k - [j not listed] r p_j / P),
  * g = grad_loss[r] (scale it by T^2 for the customary weight).  A row with no
- * id in range has loss and gradient 0.  stats: eight binary32 numbers a row. */
+ * id in range has loss and gradient 0.  The workspace and stats (eight
+ * binary32 numbers a row) serve as above; loss may be NULL. */
 size_t flashopt_distill_workspace_bytes(int32_t type, int64_t rows, int64_t vocab);
 int flashopt_distill(const void* logits, int32_t type, int64_t rows, int64_t vocab,
                      int64_t stride, double temperature, const int64_t* top_id,
@@ -110,8 +113,7 @@ int flashopt_distill_grad(const void* logits, int32_t type, int64_t rows, int64_
                           int64_t stride, double temperature, const int64_t* top_id,
                           const float* top_logprob, int32_t top, int32_t tail,
                           const float* grad_loss, void* workspace, size_t workspace_bytes,
-                          float* loss, float* stats, void* grad, int64_t grad_stride,
-                          void* stream);
+                          float* loss, void* grad, int64_t grad_stride, void* stream);
 
 /* ---- 8-bit rows -------------------------------------------------------------
  *

@@ -51,10 +51,10 @@ def test_logprob_gradient_refusals():
     assert back(rows=0) == 0 and back(grad=None) == -1 and back(st=None) == -1 and back(targets=None) == -1
     assert back(gs=99) == -2 and back(grad=ODD) == -3 and back(gl=P(0x10002)) == -3 and back(gh=ODD) == -3
 
-    def both(grad=A, gs=100000, st=A, targets=A, gl=A, ws=A, wsb=1 << 20, lp=A):
-        return F.lib().flashopt_logprob_grad(A, BF16, 4, 100000, 100000, 1.0, targets, gl, None, ws, wsb, lp, A, st, grad, gs, None)
-    assert both(grad=None) == -1 and both(st=None) == -1 and both(targets=None) == -1
-    assert both(gs=99) == -2 and both(wsb=1) == -6 and both(ws=None) == -1 and both(st=P(0x10004)) == -3
+    def both(grad=A, gs=100000, targets=A, gl=A, ws=A, wsb=1 << 20, lp=A):
+        return F.lib().flashopt_logprob_grad(A, BF16, 4, 100000, 100000, 1.0, targets, gl, None, ws, wsb, lp, A, grad, gs, None)
+    assert both(grad=None) == -1 and both(targets=None) == -1 and both(gl=P(0x10002)) == -3
+    assert both(gs=99) == -2 and both(wsb=1) == -6 and both(ws=None) == -1 and both(lp=ODD) == -3
 
 
 def test_distill_refusals():
@@ -71,7 +71,7 @@ def test_distill_refusals():
     assert back(gs=1) == -2 and back(top=0) == -4 and back(grad=ODD) == -3 and back(g=ODD) == -3
 
     def both(g=A, grad=A, wsb=1 << 20, top=4, tail=0):
-        return F.lib().flashopt_distill_grad(A, BF16, 4, 100000, 100000, 1.0, A, A, top, tail, g, A, wsb, A, A, grad,
+        return F.lib().flashopt_distill_grad(A, BF16, 4, 100000, 100000, 1.0, A, A, top, tail, g, A, wsb, A, grad,
                                              100000, None)
     assert both(g=None) == -1 and both(grad=None) == -1 and both(wsb=1) == -6 and both(top=0) == -4 and both(tail=-1) == -4
 
