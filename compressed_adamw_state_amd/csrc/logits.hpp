@@ -271,10 +271,8 @@ struct Upstream {                                // and where the gradient goes
     int64_t stride;
 };
 
-// logits_row.hip: loss and gradient of rows that fit a block's registers;
-// false if these rows are to be cut into segments instead.
+// logits_row.hip: log probability and gradient of rows that fit a block's
+// registers; false if these rows are to be cut into segments instead.
 bool launch_rows_prob(const Rows& a, const ProbOut& out, const Upstream& g, hipStream_t st);
-bool launch_rows_distill(const Rows& a, const DistillIn& list, float* loss, const Upstream& g,
-                         hipStream_t st);
 
 }  // namespace flashopt
