@@ -22,60 +22,113 @@ static inline int64_t ld_of(int64_t cols) { return (cols + kLdStep - 1) / kLdSte
 
 // rne(127 x / a), decided as by exact division.  r = RN(127 / a): x r is within
 // 2^-22 of the quotient relative to it, below 2^-15 absolutely, so only a value
-// that lies within 2^-12 of a border between two codes needs more: there the
+// that lies within 2^-14 of a border between two codes needs more: there the
 // quotient is formed in binary64, whose rounding error (2^-46 at most here)
 // moves it over no border unless an FP32 row holds a value that close to one.
 __device__ __forceinline__ int row_code(float x, float a, float r) {
     const float v = x * r;
     float q = __builtin_rintf(v);
-    if (__builtin_fabsf(v - q) > 0.5f - 0x1p-12f) q = (float)__builtin_rint((double)x * 127.0 / (double)a);
+    if (__builtin_fabsf(v - q) > 0.5f - 0x1p-14f) q = (float)__builtin_rint((double)x * 127.0 / (double)a);
     return (int)fminf(fmaxf(q, -127.0f), 127.0f);
 }
 
-// One block per row; load(j) gives element j as binary32.
-template <typename Load>
-__device__ __forceinline__ void quantize_row(Load load, int64_t cols, int64_t ld, int8_t* codes,
-                                             float* scale) {
-    __shared__ float red[kWavesPerBlock];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    // the largest magnitude as an unsigned pattern: infinities and NaN rank above
-    uint32_t top = 0;
-    for (int64_t j = threadIdx.x; j < cols; j += kBlock)
-        top = max(top, as_u32(load(j)) & 0x7FFFFFFFu);
+// A row's largest magnitude, as a pattern: infinities and NaN rank above all.
+struct RowScale {
+    float a, r;
+    bool bad, small;
+    __device__ __forceinline__ explicit RowScale(uint32_t top) : a(as_f32(top)) {
+        bad = top >= 0x7F800000u;
+        // below 2^-100, 127 / a overflows or x r is of a subnormal: binary64 for all
+        small = a < 0x1p-100f;
+        r = small || bad ? 0.0f : 127.0f / a;
+    }
+    __device__ __forceinline__ int code(float x) const {
+        if (bad || a == 0.0f) return 0;
+        return small ? (int)__builtin_rint((double)x * 127.0 / (double)a) : row_code(x, a, r);
+    }
+    __device__ __forceinline__ float scale() const { return bad ? NAN : a / 127.0f; }
+};
+
+// the largest of a block's patterns; red: one word per wave
+template <int kWaves>
+__device__ __forceinline__ uint32_t block_max(uint32_t top, uint32_t* red) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
-    if (lane == 0) red[wave] = as_f32(top);
+    if (kWaves == 1) return top;
+    if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWavesPerBlock; ++w) top = max(top, as_u32(red[w]));
-    const bool bad = top >= 0x7F800000u;
-    const float a = as_f32(top);
-    // a below 2^-100: x r would overflow or be of a subnormal; every code in binary64
-    const bool small = a < 0x1p-100f;
-    const float r = small || bad ? 0.0f : 127.0f / a;
-    for (int64_t j = threadIdx.x; j < ld; j += kBlock) {
-        int q = 0;
-        if (j < cols && !bad && a > 0.0f) {
-            const float x = load(j);
-            q = small ? (int)__builtin_rint((double)x * 127.0 / (double)a) : row_code(x, a, r);
-        }
-        codes[j] = (int8_t)q;
-    }
-    if (threadIdx.x == 0) *scale = bad ? NAN : a / 127.0f;
+    for (int w = 0; w < kWaves; ++w) top = max(top, red[w]);
+    return top;
 }
 
+// The codes of one 16-byte word, from entry j of its row on; entries past the
+// row are 0.
 template <int kType>
-__global__ __launch_bounds__(kBlock) void quantize_rows_kernel(const typename Elem<kType>::T* x,
+__device__ __forceinline__ void word_codes(const u32x4& v, int64_t j, int64_t cols,
+                                           const RowScale& S, int8_t* out) {
+    constexpr int E = Elem<kType>::kE;
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int q = j + e < cols ? S.code(Elem<kType>::get(v, e)) : 0;
+        w[e / 4] |= ((uint32_t)q & 0xFFu) << (8 * (e % 4));
+    }
+    if (E == 8) *reinterpret_cast<u32x2*>(out + j) = u32x2{w[0], w[1]};
+    else *reinterpret_cast<uint32_t*>(out + j) = w[0];
+}
+
+// One block of kWaves waves per row, the row in registers: read once.
+// 8192 rows of 4096 in BF16: 24 us, 4.2 TB/s; element by element in two passes 80.
+template <int kType, int kWaves, int kVecs>
+__global__ __launch_bounds__(kWaves * kWave) void quantize_rows_kernel(
+    const typename Elem<kType>::T* x, int64_t cols, int64_t stride, int64_t ld, int8_t* codes,
+    float* scale) {
+    constexpr int E = Elem<kType>::kE;
+    __shared__ uint32_t red[kWaves];
+    const int64_t row = blockIdx.x;
+    const typename Elem<kType>::T* p = x + row * stride;
+    u32x4 r[kVecs];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) r[i] = load_vec<kType>(p, i * kWaves * kWave + threadIdx.x, cols, 0);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+        for (int e = 0; e < E; ++e) top = max(top, as_u32(Elem<kType>::get(r[i], e)) & 0x7FFFFFFFu);
+    const RowScale S(block_max<kWaves>(top, red));
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        const int64_t j = ((int64_t)i * kWaves * kWave + threadIdx.x) * E;
+        if (j < ld) word_codes<kType>(r[i], j, cols, S, codes + row * ld);
+    }
+    if (threadIdx.x == 0) scale[row] = S.scale();
+}
+
+// Longer rows: read twice.
+template <int kType>
+__global__ __launch_bounds__(kBlock) void quantize_long_kernel(const typename Elem<kType>::T* x,
                                                                int64_t cols, int64_t stride,
                                                                int64_t ld, int8_t* codes,
                                                                float* scale) {
+    constexpr int E = Elem<kType>::kE;
+    __shared__ uint32_t red[kWavesPerBlock];
     const int64_t row = blockIdx.x;
     const typename Elem<kType>::T* p = x + row * stride;
-    quantize_row([&](int64_t j) { return Elem<kType>::up(p[j]); }, cols, ld, codes + row * ld,
-                 scale + row);
+    uint32_t top = 0;
+    for (int64_t w = threadIdx.x; w * E < cols; w += kBlock) {
+        const u32x4 v = load_vec<kType>(p, w, cols, 0);
+#pragma unroll
+        for (int e = 0; e < E; ++e) top = max(top, as_u32(Elem<kType>::get(v, e)) & 0x7FFFFFFFu);
+    }
+    const RowScale S(block_max<kWavesPerBlock>(top, red));
+    for (int64_t w = threadIdx.x; w * E < ld; w += kBlock)
+        word_codes<kType>(load_vec<kType>(p, w, cols, 0), w * E, cols, S, codes + row * ld);
+    if (threadIdx.x == 0) scale[row] = S.scale();
 }
 
-// the same from a tensor's state: the rebuilt master weight, element by element
+// The same from a tensor's state: the rebuilt master weight, element by
+// element (an export; rows start at any element of the state's blocks).
 template <int kOpt, bool kFp32>
 __global__ __launch_bounds__(kBlock) void quantize_state_kernel(DevTensor d, int64_t cols,
                                                                 int64_t ld, int8_t* codes,
@@ -90,7 +143,13 @@ __global__ __launch_bounds__(kBlock) void quantize_state_kernel(DevTensor d, int
         }
         return unsplit(T.theta[e], (int32_t)(int8_t)*code_at<kOpt>(T, e, kRho));
     };
-    quantize_row(load, cols, ld, codes + row * ld, scale + row);
+    __shared__ uint32_t red[kWavesPerBlock];
+    uint32_t top = 0;
+    for (int64_t j = threadIdx.x; j < cols; j += kBlock) top = max(top, as_u32(load(j)) & 0x7FFFFFFFu);
+    const RowScale S(block_max<kWavesPerBlock>(top, red));
+    for (int64_t j = threadIdx.x; j < ld; j += kBlock)
+        codes[row * ld + j] = (int8_t)(j < cols ? S.code(load(j)) : 0);
+    if (threadIdx.x == 0) scale[row] = S.scale();
 }
 
 // ---- the product: tiles -----------------------------------------------------------
@@ -397,11 +456,20 @@ static int check_codes(const void* codes, const void* scale) {
 
 static int launch_quantize(const void* x, int32_t type, int64_t rows, int64_t cols, int64_t stride,
                            int8_t* codes, float* scale, hipStream_t st) {
+    const int64_t ld = ld_of(cols);
     return by_type(type, [&](auto k) {
-        constexpr int kType = decltype(k)::value;
-        hipLaunchKernelGGL((quantize_rows_kernel<kType>), dim3((unsigned)rows), dim3(kBlock), 0, st,
-                           (const typename Elem<kType>::T*)x, cols, stride, ld_of(cols), codes,
-                           scale);
+        constexpr int kType = decltype(k)::value, E = Elem<kType>::kE;
+        const auto* p = (const typename Elem<kType>::T*)x;
+        const dim3 grid((unsigned)rows);
+        // the fewest waves and words that hold a row
+        if (ld <= 2 * kWave * E)
+            hipLaunchKernelGGL((quantize_rows_kernel<kType, 1, 2>), grid, dim3(kWave), 0, st, p, cols, stride, ld, codes, scale);
+        else if (ld <= 2 * kBlock * E)
+            hipLaunchKernelGGL((quantize_rows_kernel<kType, 4, 2>), grid, dim3(kBlock), 0, st, p, cols, stride, ld, codes, scale);
+        else if (ld <= 8 * kBlock * E)
+            hipLaunchKernelGGL((quantize_rows_kernel<kType, 4, 8>), grid, dim3(kBlock), 0, st, p, cols, stride, ld, codes, scale);
+        else
+            hipLaunchKernelGGL((quantize_long_kernel<kType>), grid, dim3(kBlock), 0, st, p, cols, stride, ld, codes, scale);
     });
 }
 
