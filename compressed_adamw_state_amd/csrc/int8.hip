@@ -165,8 +165,8 @@ __global__ __launch_bounds__(kBlock) void quantize_state_kernel(DevTensor d, int
 //   step 3:    the next stage's first fragments are read.
 // Each step reads the next step's fragments, and its products are spread over
 // what it issues (sched_group_barrier).  A row of 128 bytes keeps its word c
-// at c ^ (row & 7), so that the 8 rows read or the 8 words written at a time
-// lie in different banks.
+// at c ^ (row / 2 & 7): the 16 rows read at a time, or the two rows of 8 words
+// written, lie in all 64 banks.
 constexpr int kStage = 128;
 
 template <int kType, int FN, int FM, int WN, int WM>
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(WN * WM * kWave, 1) void tile_kernel(
         const int g = r < S::BN ? min(r, nlast) : min(r - S::BN, mlast);
         off[i] = (uint32_t)g * (uint32_t)ld + c0 * 16;
     }
-    const int wslot = r0 * kStage + ((c0 ^ (r0 & 7)) * 16);
+    const int wslot = r0 * kStage + ((c0 ^ (r0 / 2 & 7)) * 16);
     i32x4 g[S::kLoads];
     constexpr int kHalf = S::kLoads / 2;
     auto fetch = [&](int s, int from, int to) {
@@ -244,7 +244,7 @@ __global__ __launch_bounds__(WN * WM * kWave, 1) void tile_kernel(
     const int rb = (S::BN + wm * FM * 32 + (lane & 31)) * kStage;
     int slot[4];
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) slot[ks] = ((ks * 2 + (lane >> 5)) ^ (lane & 7)) * 16;
+    for (int ks = 0; ks < 4; ++ks) slot[ks] = ((ks * 2 + (lane >> 5)) ^ (lane / 2 & 7)) * 16;
     auto read = [&](int p, int s, int ks) {
         const int8_t* d = lds + (s & 1) * S::kStageBytes + slot[ks];
 #pragma unroll
@@ -507,7 +507,7 @@ static int launch_matmul(const int8_t* a, const float* a_scale, const int8_t* b,
         else if (((n + 255) / 256) * ((m + 255) / 256) < 200)
             launch_tile<kType, 2, 2, 2, 2>(a, a_scale, b, b_scale, bi, m, n, ld, o, out_stride, st);
         else
-            launch_tile<kType, 4, 4, 2, 2>(a, a_scale, b, b_scale, bi, m, n, ld, o, out_stride, st);
+            launch_tile<kType, 2, 4, 4, 2>(a, a_scale, b, b_scale, bi, m, n, ld, o, out_stride, st);
     });
 }
 
