@@ -167,6 +167,10 @@ __global__ __launch_bounds__(kBlock) void quantize_state_kernel(DevTensor d, int
 // what it issues (sched_group_barrier).  A row of 128 bytes keeps its word c
 // at c ^ (row / 2 & 7): the 16 rows read at a time, or the two rows of 8 words
 // written, lie in all 64 banks.
+//
+// Blocks stay and take tile after tile; the stages run on over a tile's end,
+// so that the next tile's first stages are loaded while this one's last
+// products and its output are under way.
 constexpr int kStage = 128;
 
 template <int kType, int FN, int FM, int WN, int WM>
@@ -176,26 +180,39 @@ struct Tile {
     static constexpr int kStageBytes = (BN + BM) * kStage;
     static constexpr int kLoads = kStageBytes / 16 / kThreads;
     static constexpr int kRowsPerLoad = kThreads / 8;
-    static constexpr int kOutPad = 16;           // bytes behind each row of the output strip
-    static constexpr size_t kLds = 2 * kStageBytes;
+    // a tile's scales and bias: BN weight scales, BN biases, BM token scales
+    static constexpr int kScales = 2 * BN + BM, kScalesEach = (kScales + kThreads - 1) / kThreads;
+    static constexpr int kPlace = kScalesEach * kThreads;
+    static constexpr size_t kLds = 2 * kStageBytes + 2 * kPlace * sizeof(float);
+    // blocks that a CU holds (160 KB of LDS)
+    static constexpr int kBlocks = kLds > 80 * 1024 ? 1 : 2;
 };
 
-// Which tile a block takes.  Blocks go to the 8 XCDs by turns; each XCD gets a
-// run of tiles of its own, ordered in columns of at most 8 token tiles, so that
-// the tiles an XCD works on at a time share rows in its L2.
-__device__ __forceinline__ void tile_of(uint32_t block, uint32_t tn, uint32_t tm, uint32_t& n,
+// Tile t of the order in which blocks take them.  Blocks go to the 8 XCDs by
+// turns; each XCD gets a run of tiles of its own, ordered in columns of at
+// most 8 token tiles, so that the tiles an XCD works on at a time share rows in
+// its L2.
+__device__ __forceinline__ void tile_of(uint32_t t, uint32_t tn, uint32_t tm, uint32_t& n,
                                         uint32_t& m) {
-    const uint32_t total = tn * tm, xcd = block % 8, k = block / 8;
+    const uint32_t total = tn * tm, xcd = t % 8, k = t / 8;
     const uint32_t q = total / 8, r = total % 8;
-    const uint32_t t = xcd * q + (xcd < r ? xcd : r) + k;
-    const uint32_t group = 8 * tn, g = t / group, in = t % group;
+    const uint32_t u = xcd * q + (xcd < r ? xcd : r) + k;
+    const uint32_t group = 8 * tn, g = u / group, in = u % group;
     const uint32_t high = tm - g * 8 < 8 ? tm - g * 8 : 8;
     m = g * 8 + in % high;
     n = in / high;
 }
 
+// four values rounded to a 16-bit type
+template <int kType>
+__device__ __forceinline__ u32x2 pack4(const float* y) {
+    const float z[8] = {y[0], y[1], y[2], y[3], 0.0f, 0.0f, 0.0f, 0.0f};
+    const u32x4 v = pack<kType>(z);
+    return u32x2{v[0], v[1]};
+}
+
 template <int kType, int FN, int FM, int WN, int WM>
-__global__ __launch_bounds__(WN * WM * kWave, 1) void tile_kernel(
+__global__ __launch_bounds__(WN * WM * kWave, 2) void tile_kernel(
     const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
     const typename Elem<kType>::T* bias, int64_t m, int64_t n, int32_t ld, uint32_t tn, uint32_t tm,
     typename Elem<kType>::T* out, int64_t out_stride) {
@@ -204,37 +221,55 @@ __global__ __launch_bounds__(WN * WM * kWave, 1) void tile_kernel(
     extern __shared__ __attribute__((aligned(16))) int8_t lds[];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int wn = wave % WN, wm = wave / WN;
-    uint32_t in_, im_;
-    tile_of(blockIdx.x, tn, tm, in_, im_);
-    const int64_t n0 = (int64_t)in_ * S::BN, m0 = (int64_t)im_ * S::BM;
-    const int8_t* wbase = b + n0 * ld;
-    const int8_t* xbase = a + m0 * ld;
-    const int nlast = (int)(n - n0 < S::BN ? n - n0 : S::BN) - 1;
-    const int mlast = (int)(m - m0 < S::BM ? m - m0 : S::BM) - 1;
+    const int stages = ld / kStage;
+    const uint32_t total = tn * tm;
 
-    // this thread's words of a stage: row r0 + i * kRowsPerLoad, word tid % 8
+    // What is loaded next: a stage of a tile (behind the last tile its last
+    // stage again).  This thread's words: row r0 + i * kRowsPerLoad, word tid % 8.
     const int r0 = tid / 8, c0 = tid % 8;
+    const int8_t *wbase, *xbase;
     uint32_t off[S::kLoads];
+    uint32_t ftile = blockIdx.x;
+    int fstage = 0;
+    auto aim = [&](uint32_t t) {
+        uint32_t in, im;
+        tile_of(t, tn, tm, in, im);
+        const int64_t n0 = (int64_t)in * S::BN, m0 = (int64_t)im * S::BM;
+        wbase = b + n0 * ld;
+        xbase = a + m0 * ld;
+        const int nlast = (int)(n - n0 < S::BN ? n - n0 : S::BN) - 1;
+        const int mlast = (int)(m - m0 < S::BM ? m - m0 : S::BM) - 1;
 #pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) {
-        const int r = r0 + i * S::kRowsPerLoad;
-        // rows past the end read the last row; their products are not stored
-        const int g = r < S::BN ? min(r, nlast) : min(r - S::BN, mlast);
-        off[i] = (uint32_t)g * (uint32_t)ld + c0 * 16;
-    }
+        for (int i = 0; i < S::kLoads; ++i) {
+            const int r = r0 + i * S::kRowsPerLoad;
+            // rows past the end read the last row; their products are not stored
+            const int g = r < S::BN ? min(r, nlast) : min(r - S::BN, mlast);
+            off[i] = (uint32_t)g * (uint32_t)ld + c0 * 16;
+        }
+    };
+    auto advance = [&]() {
+        if (++fstage < stages) return;
+        if (ftile + gridDim.x < total) {
+            ftile += gridDim.x;
+            fstage = 0;
+            aim(ftile);
+        } else {
+            fstage = stages - 1;
+        }
+    };
     const int wslot = r0 * kStage + ((c0 ^ (r0 / 2 & 7)) * 16);
-    i32x4 g[S::kLoads];
     constexpr int kHalf = S::kLoads / 2;
-    auto fetch = [&](int s, int from, int to) {
+    i32x4 g[S::kLoads];
+    auto fetch = [&](int from, int to) {
 #pragma unroll
         for (int i = 0; i < S::kLoads; ++i) {
             if (i < from || i >= to) continue;
-            const int8_t* p = (i * S::kRowsPerLoad < S::BN ? wbase : xbase) + (int64_t)s * kStage;
+            const int8_t* p = (i * S::kRowsPerLoad < S::BN ? wbase : xbase) + (int64_t)fstage * kStage;
             g[i] = *(const i32x4*)(p + off[i]);
         }
     };
-    auto put = [&](int s, int from, int to) {
-        int8_t* d = lds + (s & 1) * S::kStageBytes + wslot;
+    auto put = [&](int half, int from, int to) {
+        int8_t* d = lds + half * S::kStageBytes + wslot;
 #pragma unroll
         for (int i = 0; i < S::kLoads; ++i)
             if (i >= from && i < to) *(i32x4*)(d + i * S::kRowsPerLoad * kStage) = g[i];
@@ -245,20 +280,14 @@ __global__ __launch_bounds__(WN * WM * kWave, 1) void tile_kernel(
     int slot[4];
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) slot[ks] = ((ks * 2 + (lane >> 5)) ^ (lane / 2 & 7)) * 16;
-    auto read = [&](int p, int s, int ks) {
-        const int8_t* d = lds + (s & 1) * S::kStageBytes + slot[ks];
+    auto read = [&](int p, int half, int ks) {
+        const int8_t* d = lds + half * S::kStageBytes + slot[ks];
 #pragma unroll
         for (int f = 0; f < FN; ++f) fa[p][f] = *(const i32x4*)(d + ra + f * 32 * kStage);
 #pragma unroll
         for (int f = 0; f < FM; ++f) fb[p][f] = *(const i32x4*)(d + rb + f * 32 * kStage);
     };
     i32x16 acc[FN][FM];
-#pragma unroll
-    for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int j = 0; j < FM; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
     auto products = [&](int p) {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
@@ -283,94 +312,117 @@ __global__ __launch_bounds__(WN * WM * kWave, 1) void tile_kernel(
         }                                                                            \
         __builtin_amdgcn_sched_barrier(0);                                           \
     } while (0)
-    const int stages = ld / kStage;
-    fetch(0, 0, S::kLoads);
+    aim(ftile);
+    fetch(0, S::kLoads);
+    advance();
     put(0, 0, S::kLoads);
-    fetch(stages > 1 ? 1 : 0, 0, S::kLoads);
+    fetch(0, S::kLoads);
+    advance();
     __syncthreads();
     read(0, 0, 0);
-    __builtin_amdgcn_sched_barrier(0);
-    for (int s = 0; s + 1 < stages; ++s) {
-        const int ahead = s + 2 < stages ? s + 2 : s + 1;        // the last: loaded, not used
-        read(1, s, 1);
-        products(0);
-        put(s + 1, 0, kHalf);
-        TILE_STEP(true, false);
-        read(0, s, 2);
-        products(1);
-        put(s + 1, kHalf, S::kLoads);
-        fetch(ahead, 0, kHalf);
-        TILE_STEP(true, true);
-        read(1, s, 3);
-        products(0);
-        fetch(ahead, kHalf, S::kLoads);
-        TILE_STEP(false, true);
-        __syncthreads();
-        read(0, s + 1, 0);
-        products(1);
-        TILE_STEP(false, false);
-    }
-#undef TILE_STEP
-    read(1, stages - 1, 1);
-    products(0);
-    read(0, stages - 1, 2);
-    products(1);
-    read(1, stages - 1, 3);
-    products(0);
-    products(1);
-    __syncthreads();                             // the strips below replace the stages
-
-    // Out through LDS, a strip of 32 tokens x FN * 32 channels of a wave at a
-    // time, so that rows are stored in 16-byte words one after another.
-    constexpr int kRowBytes = FN * 32 * (int)sizeof(T) + S::kOutPad;
-    static_assert(32 * kRowBytes * WN * WM <= (int)S::kLds, "strips fit");
-    int8_t* strip = lds + wave * (32 * kRowBytes);
-    const int64_t nw = n0 + wn * FN * 32;
-    float ws[FN][16], bs[FN][16];
+    int half = 0, turn = 0;
+    for (uint32_t t = blockIdx.x; t < total; t += gridDim.x) {
+        uint32_t in, im;
+        tile_of(t, tn, tm, in, im);
+        const int64_t n0 = (int64_t)in * S::BN, m0 = (int64_t)im * S::BM;
+        // the tile's scales and bias, to LDS before a stage's barrier (two
+        // places by turns: a wave may still read the last tile's)
+        float scales[S::kScalesEach];
 #pragma unroll
-    for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int64_t j = nw + i * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
-            ws[i][r] = j < n ? b_scale[j] : 0.0f;
-            bs[i][r] = bias && j < n ? Elem<kType>::up(bias[j]) : 0.0f;
+        for (int i = 0; i < S::kScalesEach; ++i) {
+            const int q = i * S::kThreads + tid;
+            float v = 0.0f;
+            if (q < S::BN) { if (n0 + q < n) v = b_scale[n0 + q]; }
+            else if (q < 2 * S::BN) { if (bias && n0 + q - S::BN < n) v = Elem<kType>::up(bias[n0 + q - S::BN]); }
+            else if (q < S::kScales) { if (m0 + q - 2 * S::BN < m) v = a_scale[m0 + q - 2 * S::BN]; }
+            scales[i] = v;
         }
-    constexpr int kWords = FN * 32 * (int)sizeof(T) / 16;          // 16-byte words of a strip's row
-    constexpr int E = Elem<kType>::kE;
-#pragma unroll
-    for (int f = 0; f < FM; ++f) {
-        const int64_t mf = m0 + (wm * FM + f) * 32;
-        const float s = mf + (lane & 31) < m ? a_scale[mf + (lane & 31)] : 0.0f;
+        float* place = (float*)(lds + 2 * S::kStageBytes) + turn * S::kPlace;
+        turn ^= 1;
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; r += 4) {
-                float y[4];
+            for (int j = 0; j < FM; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    y[e] = (float)acc[i][f][r + e] * (s * ws[i][r + e]);
-                    if (bias) y[e] += bs[i][r + e];
-                }
-                int8_t* d = strip + (lane & 31) * kRowBytes +
-                            (i * 32 + 8 * (r / 4) + 4 * (lane >> 5)) * (int)sizeof(T);
-                if (kType == FLASHOPT_FP32) {
-                    *(u32x4*)d = u32x4{as_u32(y[0]), as_u32(y[1]), as_u32(y[2]), as_u32(y[3])};
-                } else {
-                    *(u32x2*)d = u32x2{(uint32_t)Elem<kType>::down(y[0]) | ((uint32_t)Elem<kType>::down(y[1]) << 16),
-                                       (uint32_t)Elem<kType>::down(y[2]) | ((uint32_t)Elem<kType>::down(y[3]) << 16)};
-                }
-            }
-        // the strip is this wave's own: its writes come before its reads
-        __builtin_amdgcn_wave_barrier();
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+        __builtin_amdgcn_sched_barrier(0);
+        for (int s = 0; s < stages; ++s) {
+            read(1, half, 1);
+            products(0);
+            put(half ^ 1, 0, kHalf);
+            TILE_STEP(true, false);
+            read(0, half, 2);
+            products(1);
+            put(half ^ 1, kHalf, S::kLoads);
+            fetch(0, kHalf);
+            TILE_STEP(true, true);
+            read(1, half, 3);
+            products(0);
+            fetch(kHalf, S::kLoads);
+            TILE_STEP(false, true);
+            advance();
+            // each stage again: a branch for one of them would double the loop
 #pragma unroll
-        for (int q = 0; q < 32 * kWords / kWave; ++q) {
-            const int at = q * kWave + lane, row = at / kWords, word = at % kWords;
-            const u32x4 v = *(const u32x4*)(strip + row * kRowBytes + word * 16);
-            const int64_t i = mf + row, j = nw + word * E;
-            if (i < m && j < n) store_vec<kType>(out + i * out_stride + nw, word, n - nw, v);
+            for (int i = 0; i < S::kScalesEach; ++i) place[i * S::kThreads + tid] = scales[i];
+            __syncthreads();
+            read(0, half ^ 1, 0);
+            products(1);
+            TILE_STEP(false, false);
+            half ^= 1;
         }
-        __builtin_amdgcn_wave_barrier();
+
+        // Out through the stage's half of LDS that has just been read for the last
+        // time, a strip of kStrip tokens x FN * 32 channels of a wave at a time,
+        // so that whole lines are stored.  The loads under way are waited for
+        // first: later it would be for the stores as well.
+        __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0)
+        constexpr int kRowBytes = FN * 32 * (int)sizeof(T) + 16;
+        constexpr int kSpace = S::kStageBytes / (WN * WM), kStrip = kSpace >= 32 * kRowBytes ? 32 : 16;
+        static_assert(kStrip * kRowBytes <= kSpace, "strips fit");
+        int8_t* strip = lds + (half ^ 1) * S::kStageBytes + wave * kSpace;
+        const int64_t nw = n0 + wn * FN * 32;
+        const float *ws = place + wn * FN * 32, *bs = ws + S::BN, *as = place + 2 * S::BN + wm * FM * 32;
+        constexpr int kWords = FN * 32 * (int)sizeof(T) / 16;    // 16-byte words of a strip's row
+        constexpr int E = Elem<kType>::kE;
+#pragma unroll
+        for (int f = 0; f < FM; ++f) {
+            const int64_t mf = m0 + (wm * FM + f) * 32;
+            const float s = as[f * 32 + (lane & 31)];
+#pragma unroll
+            for (int part = 0; part < 32; part += kStrip) {
+                if (kStrip == 32 || (lane & 31) / kStrip == part / kStrip)
+#pragma unroll
+                    for (int c = 0; c < FN; ++c)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int j = c * 32 + 8 * q + 4 * (lane >> 5);
+                            float y[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                y[e] = (float)acc[c][f][4 * q + e] * (s * ws[j + e]) + bs[j + e];
+                            int8_t* d = strip + ((lane & 31) - part) * kRowBytes + j * (int)sizeof(T);
+                            if (kType == FLASHOPT_FP32)
+                                *(u32x4*)d = u32x4{as_u32(y[0]), as_u32(y[1]), as_u32(y[2]), as_u32(y[3])};
+                            else
+                                *(u32x2*)d = pack4<kType>(y);
+                        }
+                // the strip is this wave's own: its writes come before its reads
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int q = 0; q < kStrip * kWords / kWave; ++q) {
+                    const int at = q * kWave + lane, row = at / kWords, word = at % kWords;
+                    const u32x4 v = *(const u32x4*)(strip + row * kRowBytes + word * 16);
+                    const int64_t i = mf + part + row, j = nw + word * E;
+                    if (i < m && j + E <= n) __builtin_nontemporal_store(v, (u32x4_any*)(out + i * out_stride + j));
+                    else if (i < m && j < n) store_vec<kType>(out + i * out_stride + nw, word, n - nw, v);
+                }
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
+        __syncthreads();                         // the strips make way for a stage
+        __builtin_amdgcn_sched_barrier(0);
     }
+#undef TILE_STEP
 }
 
 // ---- the product: few tokens ------------------------------------------------------
@@ -480,7 +532,8 @@ static void launch_tile(const int8_t* a, const float* a_scale, const int8_t* b,
                         hipStream_t st) {
     typedef Tile<kType, FN, FM, WN, WM> S;
     const int64_t tn = (n + S::BN - 1) / S::BN, tm = (m + S::BM - 1) / S::BM;
-    hipLaunchKernelGGL((tile_kernel<kType, FN, FM, WN, WM>), dim3((unsigned)(tn * tm)),
+    const int64_t most = 256 * S::kBlocks, blocks = tn * tm < most ? tn * tm : most;
+    hipLaunchKernelGGL((tile_kernel<kType, FN, FM, WN, WM>), dim3((unsigned)blocks),
                        dim3(S::kThreads), S::kLds, st, a, a_scale, b, b_scale, bias, m, n,
                        (int32_t)ld, (uint32_t)tn, (uint32_t)tm, out, out_stride);
 }
