@@ -96,20 +96,22 @@ def test_int8_refusals():
     assert state(t=F.Tensor(100, A, None, A, None)) == -1 and state(t=F.Tensor(0, None, None, None, None)) == 0
     assert state(t=F.Tensor(100, A, P(0x10008), A, None)) == -3
 
-    def prod(a=A, sa=A, b=A, sb=A, bias=None, m=4, n=5, k=100, out=A, type=BF16, os=5, ws=A, wsb=1 << 24):
-        return lib.flashopt_int8_matmul(a, sa, b, sb, bias, m, n, k, out, type, os, ws, wsb, None)
+    def prod(a=A, sa=A, b=A, sb=A, bias=None, m=4, n=5, k=100, out=A, type=BF16, os=5):
+        return lib.flashopt_int8_matmul(a, sa, b, sb, bias, m, n, k, out, type, os, None)
     assert prod(m=0) == 0 and prod(n=0) == 0 and prod(m=-1) == -2 and prod(k=0) == -2 and prod(k=131073) == -2
     assert prod(os=4) == -2 and prod(type=3) == -4 and prod(n=(1 << 24) + 1, os=1 << 25) == -2
     assert prod(a=None) == -1 and prod(sa=None) == -1 and prod(b=None) == -1 and prod(sb=None) == -1
     assert prod(out=None) == -1 and prod(a=P(0x10008)) == -3 and prod(b=P(0x10004)) == -3
     assert prod(out=ODD) == -3 and prod(bias=ODD) == -3
 
-    def lin(x=A, type=BF16, m=4, k=100, xs=100, w=A, ws=A, bias=None, n=5, out=A, os=5, work=A, wb=1 << 24):
+    def lin(x=A, type=BF16, m=9, k=100, xs=100, w=A, ws=A, bias=None, n=5, out=A, os=5, work=A, wb=1 << 24):
         return lib.flashopt_int8_linear(x, type, m, k, xs, w, ws, bias, n, out, os, work, wb, None)
     assert lin(m=0) == 0 and lin(n=0) == 0 and lin(x=None) == -1 and lin(work=None) == -1 and lin(w=None) == -1
     assert lin(xs=99) == -2 and lin(os=4) == -2 and lin(type=9) == -4 and lin(k=131073, xs=131073) == -2
     assert lin(x=ODD) == -3 and lin(wb=1) == -6 and lin(work=P(0x10010)) == -6
-    assert lib.flashopt_int8_workspace_bytes(4, 5, 0) == 0 and lib.flashopt_int8_workspace_bytes(4, 5, 100) > 0
+    assert lin(m=1, x=None) == -1 and lin(m=1, w=None) == -1 and lin(m=1, out=None) == -1 and lin(m=1, bias=ODD) == -3
+    assert lin(m=1, w=P(0x10008)) == -3 and lin(m=1, ws=P(0x10002)) == -3 and lin(m=1, out=ODD) == -3
+    assert lib.flashopt_int8_workspace_bytes(4, 5, 0) == 0 and lib.flashopt_int8_workspace_bytes(9, 5, 100) > 0
 
 
 def test_python_refusals():
