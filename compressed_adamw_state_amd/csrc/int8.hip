@@ -171,6 +171,11 @@ __global__ __launch_bounds__(kBlock) void quantize_state_kernel(DevTensor d, int
 // Blocks stay and take tile after tile; the stages run on over a tile's end,
 // so that the next tile's first stages are loaded while this one's last
 // products and its output are under way.
+//
+// kSplit: where there are few tiles, each is cut along the row into `splits`
+// pieces that count as tiles here; a piece's integer sums go to `sums` as the
+// registers hold them, 16 bytes of each lane after the other's, and
+// join_kernel adds them up and writes the output.
 constexpr int kStage = 128;
 
 template <int kType, int FN, int FM, int WN, int WM>
@@ -211,18 +216,28 @@ __device__ __forceinline__ u32x2 pack4(const float* y) {
     return u32x2{v[0], v[1]};
 }
 
-template <int kType, int FN, int FM, int WN, int WM>
+template <int kType, int FN, int FM, int WN, int WM, bool kSplit>
 __global__ __launch_bounds__(WN * WM * kWave, 2) void tile_kernel(
     const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
     const typename Elem<kType>::T* bias, int64_t m, int64_t n, int32_t ld, uint32_t tn, uint32_t tm,
-    typename Elem<kType>::T* out, int64_t out_stride) {
+    uint32_t splits, i32x4* sums, typename Elem<kType>::T* out, int64_t out_stride) {
     typedef Tile<kType, FN, FM, WN, WM> S;
     typedef typename Elem<kType>::T T;
     extern __shared__ __attribute__((aligned(16))) int8_t lds[];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int wn = wave % WN, wm = wave / WN;
-    const int stages = ld / kStage;
-    const uint32_t total = tn * tm;
+    const int row_stages = ld / kStage;
+    const uint32_t total = tn * tm * (kSplit ? splits : 1);
+    // a tile's first stage of its row, and its stages
+    auto stages_of = [&](uint32_t t, int& from) {
+        if (!kSplit) {
+            from = 0;
+            return row_stages;
+        }
+        const uint32_t q = t % splits;
+        from = (int)(row_stages * q / splits);
+        return (int)(row_stages * (q + 1) / splits) - from;
+    };
 
     // What is loaded next: a stage of a tile (behind the last tile its last
     // stage again).  This thread's words: row r0 + i * kRowsPerLoad, word tid % 8.
@@ -230,13 +245,15 @@ __global__ __launch_bounds__(WN * WM * kWave, 2) void tile_kernel(
     const int8_t *wbase, *xbase;
     uint32_t off[S::kLoads];
     uint32_t ftile = blockIdx.x;
-    int fstage = 0;
+    int fstage = 0, fstages;
     auto aim = [&](uint32_t t) {
         uint32_t in, im;
-        tile_of(t, tn, tm, in, im);
+        tile_of(kSplit ? t / splits : t, tn, tm, in, im);
         const int64_t n0 = (int64_t)in * S::BN, m0 = (int64_t)im * S::BM;
-        wbase = b + n0 * ld;
-        xbase = a + m0 * ld;
+        int from;
+        fstages = stages_of(t, from);
+        wbase = b + n0 * ld + from * kStage;
+        xbase = a + m0 * ld + from * kStage;
         const int nlast = (int)(n - n0 < S::BN ? n - n0 : S::BN) - 1;
         const int mlast = (int)(m - m0 < S::BM ? m - m0 : S::BM) - 1;
 #pragma unroll
@@ -248,13 +265,13 @@ __global__ __launch_bounds__(WN * WM * kWave, 2) void tile_kernel(
         }
     };
     auto advance = [&]() {
-        if (++fstage < stages) return;
+        if (++fstage < fstages) return;
         if (ftile + gridDim.x < total) {
             ftile += gridDim.x;
             fstage = 0;
             aim(ftile);
         } else {
-            fstage = stages - 1;
+            fstage = fstages - 1;
         }
     };
     const int wslot = r0 * kStage + ((c0 ^ (r0 / 2 & 7)) * 16);
@@ -335,11 +352,11 @@ __global__ __launch_bounds__(WN * WM * kWave, 2) void tile_kernel(
 #pragma unroll
         for (int i = 0; i < S::kScalesEach; ++i) places[place * S::kPlace + i * S::kThreads + tid] = scales[i];
     };
-    load_scales(blockIdx.x);
+    if (!kSplit) load_scales(blockIdx.x);
     aim(ftile);
     fetch(0, S::kLoads);
     advance();
-    put_scales(0);
+    if (!kSplit) put_scales(0);
     put(0, 0, S::kLoads);
     fetch(0, S::kLoads);
     advance();
@@ -348,9 +365,11 @@ __global__ __launch_bounds__(WN * WM * kWave, 2) void tile_kernel(
     int half = 0, turn = 0;
     for (uint32_t t = blockIdx.x; t < total; t += gridDim.x) {
         uint32_t in, im;
-        tile_of(t, tn, tm, in, im);
+        tile_of(kSplit ? t / splits : t, tn, tm, in, im);
         const int64_t n0 = (int64_t)in * S::BN, m0 = (int64_t)im * S::BM;
-        load_scales(t + gridDim.x < total ? t + gridDim.x : t);
+        if (!kSplit) load_scales(t + gridDim.x < total ? t + gridDim.x : t);
+        int from;
+        const int stages = stages_of(t, from);
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -380,6 +399,19 @@ __global__ __launch_bounds__(WN * WM * kWave, 2) void tile_kernel(
             half ^= 1;
         }
 
+        if constexpr (kSplit) {
+            i32x4* d = sums + (int64_t)t * (FN * FM * 4 * S::kThreads) + tid;
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        d[((i * FM + j) * 4 + q) * S::kThreads] =
+                            i32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+            __builtin_amdgcn_sched_barrier(0);
+            continue;
+        }
         // Out through the stage's half of LDS that has just been read for the last
         // time, a strip of kStrip tokens x FN * 32 channels of a wave at a time,
         // so that whole lines are stored.  The loads under way are waited for
@@ -435,6 +467,43 @@ __global__ __launch_bounds__(WN * WM * kWave, 2) void tile_kernel(
         __builtin_amdgcn_sched_barrier(0);
     }
 #undef TILE_STEP
+}
+
+// The pieces of a tile added up: one block for one of its FN * FM fragments.
+template <int kType, int FN, int FM, int WN, int WM>
+__global__ __launch_bounds__(WN * WM * kWave) void join_kernel(
+    const i32x4* sums, uint32_t splits, const float* a_scale, const float* b_scale,
+    const typename Elem<kType>::T* bias, int64_t m, int64_t n, uint32_t tn, uint32_t tm,
+    typename Elem<kType>::T* out, int64_t out_stride) {
+    typedef Tile<kType, FN, FM, WN, WM> S;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const uint32_t t = blockIdx.x / (FN * FM), f = blockIdx.x % (FN * FM);
+    uint32_t in, im;
+    tile_of(t, tn, tm, in, im);
+    const int64_t i = (int64_t)im * S::BM + (wave / WN * FM + f % FM) * 32 + (lane & 31);
+    const int64_t j0 = (int64_t)in * S::BN + (wave % WN * FN + f / FM) * 32 + 4 * (lane >> 5);
+    constexpr int64_t kPiece = FN * FM * 4 * S::kThreads;
+    const i32x4* p = sums + (int64_t)t * splits * kPiece + f * 4 * S::kThreads + tid;
+    i32x4 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = p[q * S::kThreads];
+    for (uint32_t k = 1; k < splits; ++k) {
+        p += kPiece;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] += p[q * S::kThreads];
+    }
+    if (i >= m) return;
+    const float s = a_scale[i];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t j = j0 + 8 * q + e;
+            if (j >= n) continue;
+            float y = (float)v[q][e] * (s * b_scale[j]);
+            if (bias) y += Elem<kType>::up(bias[j]);
+            out[i * out_stride + j] = Elem<kType>::down(y);
+        }
 }
 
 // ---- the product: few tokens ------------------------------------------------------
@@ -635,41 +704,88 @@ static void launch_tile(const int8_t* a, const float* a_scale, const int8_t* b,
     typedef Tile<kType, FN, FM, WN, WM> S;
     const int64_t tn = (n + S::BN - 1) / S::BN, tm = (m + S::BM - 1) / S::BM;
     const int64_t most = 256 * S::kBlocks, blocks = tn * tm < most ? tn * tm : most;
-    hipLaunchKernelGGL((tile_kernel<kType, FN, FM, WN, WM>), dim3((unsigned)blocks),
+    hipLaunchKernelGGL((tile_kernel<kType, FN, FM, WN, WM, false>), dim3((unsigned)blocks),
                        dim3(S::kThreads), S::kLds, st, a, a_scale, b, b_scale, bias, m, n,
-                       (int32_t)ld, (uint32_t)tn, (uint32_t)tm, out, out_stride);
+                       (int32_t)ld, (uint32_t)tn, (uint32_t)tm, 1u, nullptr, out, out_stride);
 }
 
-static int launch_matmul(const int8_t* a, const float* a_scale, const int8_t* b,
+// How a product is done, and what of a workspace it needs.
+struct Plan {
+    enum Way { kSkinny, kSplit, kSmall, kLarge } way;
+    int skinny;                                  // 16 tokens times this
+    int64_t splits;
+    size_t sums;                                 // bytes
+};
+typedef Tile<FLASHOPT_FP32, 2, 2, 2, 2> SmallTile;
+
+static Plan plan_of(int64_t m, int64_t n, int64_t k) {
+    Plan p = {Plan::kSkinny, 0, 1, 0};
+    const int64_t stages = ld_of(k) / kStage;
+    const int64_t tn = (n + SmallTile::BN - 1) / SmallTile::BN, tm = (m + SmallTile::BM - 1) / SmallTile::BM;
+    const int64_t tiles = tn * tm, large = ((n + 255) / 256) * ((m + 255) / 256);
+    // Up to 16 tokens the weights' own rate decides.  Up to 64 the tokens read
+    // again for every 16 channels count, but tiles need channels to fill the
+    // GPU: 32 tokens, 14336 x 4096: 27.7 us here, 24.6 in tiles; 4096 x 14336: 26
+    // and, even split, 34.
+    p.skinny = m <= 16 ? 1 : m <= 32 && tn < 96 ? 2 : m <= 64 && tn < 96 ? 4 : 0;
+    if (p.skinny) return p;
+    // 4096 x 4096 x 4096 in large tiles: 64 us; 2048 x 4096 x 4096 in small ones 40
+    // for 47, 1024 x 5120 x 5120 40 for 63
+    if (large >= 200) {
+        p.way = Plan::kLarge;
+        return p;
+    }
+    p.way = Plan::kSmall;
+    // Pieces of at least 8 stages, until a block runs on each CU, if that gains:
+    // a stage takes about half a microsecond of a block alone on its CU, another
+    // launch 6, a piece's sums 1/32.  100 tokens, 4096 x 14336 (32 tiles): 34 us
+    // for 66; 1024 x 4096 (8 tiles): 20 for 24; but 128 tokens, 14336 x 4096 (112
+    // tiles): 31 for 22.
+    const int64_t q = 256 / tiles < stages / 8 ? 256 / tiles : stages / 8;
+    if (q >= 2 && stages * (q - 1) * 16 > q * (192 + tiles * q)) {
+        p.way = Plan::kSplit;
+        p.splits = q;
+        p.sums = (size_t)(tiles * q) * (SmallTile::BN * SmallTile::BM * sizeof(int));
+    }
+    return p;
+}
+
+static int launch_matmul(const Plan& plan, const int8_t* a, const float* a_scale, const int8_t* b,
                          const float* b_scale, const void* bias, int64_t m, int64_t n, int64_t k,
-                         void* out, int32_t type, int64_t out_stride, hipStream_t st) {
+                         void* out, int32_t type, int64_t out_stride, void* sums, hipStream_t st) {
     return by_type(type, [&](auto t) {
         constexpr int kType = decltype(t)::value;
         typedef typename Elem<kType>::T T;
         const int64_t ld = ld_of(k);
         const T* bi = (const T*)bias;
         T* o = (T*)out;
-        const dim3 strips((unsigned)((n + 15) / 16)), threads(kSkinnyWaves * kWave);
-        // Up to 16 tokens the weights' own rate decides.  Up to 64 the tokens read
-        // again for every 16 channels count, but tiles need channels to fill the
-        // GPU: 32 tokens, 14336 x 4096: 27.7 us here, 24.6 in tiles; 4096 x 14336:
-        // 26 and 59, 64 tokens 39 and 59.
-        const int64_t tall = (n + 127) / 128, wide = ((n + 255) / 256) * ((m + 255) / 256);
-        if (m <= 16)
-            hipLaunchKernelGGL((skinny_kernel<kType, 1>), strips, threads, 0, st, a, a_scale, b,
-                               b_scale, bi, (int)m, n, (int32_t)ld, o, out_stride);
-        else if (m <= 32 && tall < 96)
-            hipLaunchKernelGGL((skinny_kernel<kType, 2>), strips, threads, 0, st, a, a_scale, b,
-                               b_scale, bi, (int)m, n, (int32_t)ld, o, out_stride);
-        else if (m <= 64 && tall < 96)
-            hipLaunchKernelGGL((skinny_kernel<kType, 4>), strips, threads, 0, st, a, a_scale, b,
-                               b_scale, bi, (int)m, n, (int32_t)ld, o, out_stride);
-        else if (wide < 200)
-            // 2048 x 4096 x 4096: 40 us for 47, 1024 x 5120 x 5120: 40 for 63
-            launch_tile<kType, 2, 2, 2, 2>(a, a_scale, b, b_scale, bi, m, n, ld, o, out_stride, st);
-        else
-            // 4096 x 4096 x 4096: 64 us; 8192 x 14336 x 4096: 410 us, 2.35 POP/s
+        auto skinny = [&](auto mt) {
+            constexpr int MT = decltype(mt)::value;
+            hipLaunchKernelGGL((skinny_kernel<kType, MT>), dim3((unsigned)((n + 15) / 16)),
+                               dim3(kSkinnyWaves * kWave), 0, st, a, a_scale, b, b_scale, bi, (int)m,
+                               n, (int32_t)ld, o, out_stride);
+        };
+        if (plan.way == Plan::kLarge) {
             launch_tile<kType, 2, 4, 4, 2>(a, a_scale, b, b_scale, bi, m, n, ld, o, out_stride, st);
+        } else if (plan.way == Plan::kSmall) {
+            launch_tile<kType, 2, 2, 2, 2>(a, a_scale, b, b_scale, bi, m, n, ld, o, out_stride, st);
+        } else if (plan.way == Plan::kSplit) {
+            typedef SmallTile S;
+            const uint32_t tn = (uint32_t)((n + S::BN - 1) / S::BN), tm = (uint32_t)((m + S::BM - 1) / S::BM);
+            hipLaunchKernelGGL((tile_kernel<FLASHOPT_FP32, 2, 2, 2, 2, true>),
+                               dim3((unsigned)(tn * tm * plan.splits)), dim3(S::kThreads), S::kLds, st,
+                               a, a_scale, b, b_scale, nullptr, m, n, (int32_t)ld, tn, tm,
+                               (uint32_t)plan.splits, (i32x4*)sums, nullptr, 0);
+            hipLaunchKernelGGL((join_kernel<kType, 2, 2, 2, 2>), dim3(tn * tm * 4), dim3(S::kThreads),
+                               0, st, (const i32x4*)sums, (uint32_t)plan.splits, a_scale, b_scale, bi,
+                               m, n, tn, tm, o, out_stride);
+        } else if (plan.skinny == 1) {
+            skinny(std::integral_constant<int, 1>());
+        } else if (plan.skinny == 2) {
+            skinny(std::integral_constant<int, 2>());
+        } else {
+            skinny(std::integral_constant<int, 4>());
+        }
     });
 }
 
@@ -737,8 +853,14 @@ int flashopt_tensor_quantize_rows(const flashopt_tensor* t, int32_t kind, int64_
 }
 
 size_t flashopt_int8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-    if (check_matrix(m, k) || check_matrix(n, k) || few_tokens(m, n, k)) return 0;
-    return up256((size_t)(m * ld_of(k))) + up256((size_t)m * sizeof(float));
+    if (check_matrix(m, k) || check_matrix(n, k) || m == 0 || n == 0 || few_tokens(m, n, k)) return 0;
+    return up256(plan_of(m, n, k).sums) + up256((size_t)(m * ld_of(k))) +
+           up256((size_t)m * sizeof(float));
+}
+
+size_t flashopt_int8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+    if (check_matrix(m, k) || check_matrix(n, k) || m == 0 || n == 0) return 0;
+    return plan_of(m, n, k).sums;
 }
 
 static int check_product(const int8_t* a, const float* a_scale, const int8_t* b,
@@ -754,15 +876,21 @@ static int check_product(const int8_t* a, const float* a_scale, const int8_t* b,
 
 int flashopt_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b,
                          const float* b_scale, const void* bias, int64_t m, int64_t n, int64_t k,
-                         void* out, int32_t out_type, int64_t out_stride, void* stream) {
+                         void* out, int32_t out_type, int64_t out_stride, void* workspace,
+                         size_t workspace_bytes, void* stream) {
     if (!valid_type(out_type)) return FLASHOPT_ERR_ARG;
     if (check_matrix(m, k) || check_matrix(n, k) || out_stride < n || out_stride > kMaxNumel)
         return FLASHOPT_ERR_SIZE;
     if (m == 0 || n == 0) return FLASHOPT_OK;
     const int e = check_product(a, a_scale, b, b_scale, bias, out, out_type);
     if (e) return e;
-    return launch_matmul(a, a_scale, b, b_scale, bias, m, n, k, out, out_type, out_stride,
-                         (hipStream_t)stream);
+    const Plan plan = plan_of(m, n, k);
+    if (plan.sums) {
+        if (!workspace) return FLASHOPT_ERR_NULL;
+        if (workspace_bytes < plan.sums || !aligned(workspace, 256)) return FLASHOPT_ERR_WORKSPACE;
+    }
+    return launch_matmul(plan, a, a_scale, b, b_scale, bias, m, n, k, out, out_type, out_stride,
+                         workspace, (hipStream_t)stream);
 }
 
 int flashopt_int8_linear(const void* x, int32_t type, int64_t m, int64_t k, int64_t x_stride,
@@ -793,13 +921,15 @@ int flashopt_int8_linear(const void* x, int32_t type, int64_t m, int64_t k, int6
     if (!workspace) return FLASHOPT_ERR_NULL;
     if (workspace_bytes < flashopt_int8_workspace_bytes(m, n, k) || !aligned(workspace, 256))
         return FLASHOPT_ERR_WORKSPACE;
-    int8_t* codes = (int8_t*)workspace;
-    float* scale = (float*)((char*)workspace + up256((size_t)(m * ld_of(k))));
+    const Plan plan = plan_of(m, n, k);
+    int8_t* codes = (int8_t*)workspace + up256(plan.sums);
+    float* scale = (float*)(codes + up256((size_t)(m * ld_of(k))));
     const int e = check_product(codes, scale, w, w_scale, bias, out, type);
     if (e) return e;
     const int q = launch_quantize(x, type, m, k, x_stride, codes, scale, st);
     if (q) return q;
-    return launch_matmul(codes, scale, w, w_scale, bias, m, n, k, out, type, out_stride, st);
+    return launch_matmul(plan, codes, scale, w, w_scale, bias, m, n, k, out, type, out_stride,
+                         workspace, st);
 }
 
 }  // extern "C"

@@ -161,8 +161,9 @@ SIGNATURES = {
     "flashopt_tensor_quantize_rows": (ctypes.c_int, [ctypes.POINTER(Tensor), _I32, _I64, _P, _P,
                                                      _P]),
     "flashopt_int8_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "flashopt_int8_matmul_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "flashopt_int8_matmul": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _I32, _I64,
-                                            _P]),
+                                            _P, _SZ, _P]),
     "flashopt_int8_linear": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _I64,
                                             _P, _SZ, _P]),
 }
@@ -933,15 +934,18 @@ def flashopt_tensor_quantize_rows(st: TensorState, cols: int, codes, scale, stre
           _arg(scale, torch.float32, rows, dev, "scale"))
 
 
-def flashopt_int8_matmul(a, a_scale, b, b_scale, k: int, out, bias=None, stream=None) -> None:
+def flashopt_int8_matmul(a, a_scale, b, b_scale, k: int, out, bias=None, workspace=None,
+                         stream=None) -> None:
     """out [m, n] from codes a [m, ld], b [n, ld] with ld = flashopt_int8_ld(k)."""
     m, n = out.shape
     dev = out.device
     ld = lib().flashopt_int8_ld(k)
+    need = lib().flashopt_int8_matmul_workspace_bytes(m, n, k)
+    wp, wb, _ws = _scratch(workspace, need, dev, stream)
     _call("flashopt_int8_matmul", dev, stream, _arg(a, torch.int8, m * ld, dev, "a"),
           _arg(a_scale, torch.float32, m, dev, "a_scale"), _arg(b, torch.int8, n * ld, dev, "b"),
           _arg(b_scale, torch.float32, n, dev, "b_scale"), _arg(bias, out.dtype, n, dev, "bias"),
-          m, n, k, out.data_ptr(), element_type(out), row_stride(out))
+          m, n, k, out.data_ptr(), element_type(out), row_stride(out), wp, wb)
 
 
 def flashopt_int8_linear(x, w, w_scale, out, bias=None, workspace=None, stream=None) -> None:

@@ -140,12 +140,14 @@ int flashopt_tensor_quantize_rows(const flashopt_tensor* t, int32_t kind, int64_
  * a is m x k (tokens), b n x k (output channels), both as above; bias (of
  * out_type) may be NULL; out row i at element i * out_stride, out_stride >= n.
  * The sum is an exact 32-bit integer. */
+size_t flashopt_int8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
 int flashopt_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b,
                          const float* b_scale, const void* bias, int64_t m, int64_t n, int64_t k,
-                         void* out, int32_t out_type, int64_t out_stride, void* stream);
+                         void* out, int32_t out_type, int64_t out_stride, void* workspace,
+                         size_t workspace_bytes, void* stream);
 /* The linear layer: rows of x (m x k of `type`, row stride x_stride) rounded
  * to 8 bits as above, then the product, out of the same type.  The workspace
- * holds the rounded rows (0 bytes, and NULL, for a few tokens). */
+ * holds the rounded rows (both sizes may be 0, NULL will do then). */
 size_t flashopt_int8_workspace_bytes(int64_t m, int64_t n, int64_t k);
 int flashopt_int8_linear(const void* x, int32_t type, int64_t m, int64_t k, int64_t x_stride,
                          const int8_t* w, const float* w_scale, const void* bias, int64_t n,

@@ -96,13 +96,18 @@ def test_int8_refusals():
     assert state(t=F.Tensor(100, A, None, A, None)) == -1 and state(t=F.Tensor(0, None, None, None, None)) == 0
     assert state(t=F.Tensor(100, A, P(0x10008), A, None)) == -3
 
-    def prod(a=A, sa=A, b=A, sb=A, bias=None, m=4, n=5, k=100, out=A, type=BF16, os=5):
-        return lib.flashopt_int8_matmul(a, sa, b, sb, bias, m, n, k, out, type, os, None)
+    def prod(a=A, sa=A, b=A, sb=A, bias=None, m=4, n=5, k=100, out=A, type=BF16, os=5, ws=A, wsb=1 << 24):
+        return lib.flashopt_int8_matmul(a, sa, b, sb, bias, m, n, k, out, type, os, ws, wsb, None)
     assert prod(m=0) == 0 and prod(n=0) == 0 and prod(m=-1) == -2 and prod(k=0) == -2 and prod(k=131073) == -2
     assert prod(os=4) == -2 and prod(type=3) == -4 and prod(n=(1 << 24) + 1, os=1 << 25) == -2
     assert prod(a=None) == -1 and prod(sa=None) == -1 and prod(b=None) == -1 and prod(sb=None) == -1
     assert prod(out=None) == -1 and prod(a=P(0x10008)) == -3 and prod(b=P(0x10004)) == -3
     assert prod(out=ODD) == -3 and prod(bias=ODD) == -3
+
+    need = lib.flashopt_int8_matmul_workspace_bytes(100, 200, 14336)         # few tiles: cut along the row
+    cut = dict(m=100, n=200, k=14336, os=200)
+    assert need > 0 and prod(wsb=need - 1, **cut) == -6 and prod(ws=None, **cut) == -1 and prod(ws=P(0x10010), **cut) == -6
+    assert lib.flashopt_int8_matmul_workspace_bytes(4, 5, 0) == 0 and lib.flashopt_int8_matmul_workspace_bytes(4, 5, 100) == 0
 
     def lin(x=A, type=BF16, m=9, k=100, xs=100, w=A, ws=A, bias=None, n=5, out=A, os=5, work=A, wb=1 << 24):
         return lib.flashopt_int8_linear(x, type, m, k, xs, w, ws, bias, n, out, os, work, wb, None)
