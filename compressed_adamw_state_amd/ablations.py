@@ -20,9 +20,16 @@ Training"), measured on the GPU through the C ABI.
   by linear codes (the fused step's ablation kind); the page reports that
   the last diverges.
 
-Every codec operation runs in the library's kernels; the error statistics
-are plain torch reductions over their outputs, and the BF16 + BF16 baseline
-is two torch casts.  python -m compressed_adamw_state_amd.ablations prints
+* Distillation from a teacher in 8 bits: a model trained by FlashAdamW on
+  synthetic tokens is held as its BF16 weights and, straight from the
+  optimizer's state, as 8-bit rows with a scale per output channel
+  (export_int8); each form teaches a student through its top alternatives,
+  again trained by FlashAdamW.  How far the 8-bit form's answers lie from
+  the BF16 form's, and what either student learns.
+
+Every codec operation, product in 8 bits and loss runs in the library's
+kernels; the error statistics are plain torch reductions over their outputs,
+and the BF16 + BF16 baseline is two torch casts.  python -m compressed_adamw_state_amd.ablations prints
 the study as JSON.
 """
 from __future__ import annotations
@@ -189,6 +196,90 @@ def training_study(steps: int = 300, seed: int = 7, device: str = "cuda",
                                                          for k, v in hp.items()}, "loss": runs}
 
 
+def _token_task(seed: int, device: str):
+    """Synthetic tokens: x in R^64, a token of 1000 drawn from
+    softmax(2 x.A); 8192 samples to learn from and 2048 held out.  Drawn on
+    the host (seeded) and copied."""
+    g = torch.Generator().manual_seed(seed)
+    n, d, vocab = 8192 + 2048, 64, 1000
+    X = torch.randn(n, d, generator=g)
+    A = torch.randn(d, vocab, generator=g) * 2.0 / d ** 0.5
+    t = torch.multinomial(torch.softmax(X @ A, 1), 1, generator=g).squeeze(1)
+    X = X.to(torch.bfloat16)
+    return (X[:8192].to(device), t[:8192].to(device), X[8192:].to(device), t[8192:].to(device),
+            vocab, g)
+
+
+def _token_mlp(d: int, h: int, vocab: int, g: torch.Generator, device: str):
+    """Weights of a d-h-vocab ReLU MLP and its optimizer (BF16 weights)."""
+    from . import optim as O
+    ps = [torch.nn.Parameter(t.to(device)) for t in
+          (torch.randn(h, d, generator=g) / d ** 0.5, torch.randn(vocab, h, generator=g) / h ** 0.5)]
+    return ps, O.FlashAdamW(ps, lr=2e-3, weight_decay=0.01)
+
+
+def _logits(ps, x: torch.Tensor) -> torch.Tensor:
+    return torch.relu(x @ ps[0].t()) @ ps[1].t()
+
+
+def distillation_study(steps: int = 64, seed: int = 11, device: str = "cuda", top: int = 16,
+                       temperature: float = 2.0, batch: int = 1024) -> dict:
+    """A teacher, its two forms, and a student of each; mean log probabilities
+    and entropies are of the held-out samples."""
+    from . import int8 as I
+    from . import losses as L
+    X, t, Xe, te, vocab, g = _token_task(seed, device)
+
+    def batches():
+        for k in range(steps):
+            at = (k * batch) % (X.shape[0] - batch + 1)
+            yield X[at:at + batch], t[at:at + batch]
+
+    def held_out(logits):
+        r = L.token_logprobs(logits, te, top=1)
+        return {"logprob": r.logprob.mean().item(), "entropy": r.entropy.mean().item()}, r
+
+    teacher, opt = _token_mlp(64, 256, vocab, g, device)
+    weight = torch.full((batch,), -1.0 / batch, device=device)
+    for x, y in batches():
+        logits = _logits(teacher, x)
+        logits.backward(L.token_logprobs_grad(logits.detach(), y, weight).grad)
+        opt.step()
+        opt.zero_grad()
+    rows = [opt.export_int8(p) for p in teacher]
+    forms = {"bf16": lambda x: _logits(teacher, x),
+             "int8": lambda x: I.int8_linear(torch.relu(I.int8_linear(x, rows[0])), rows[1])}
+    out = {"steps": steps, "top": top, "temperature": temperature, "teacher": {}, "student": {}}
+    scale = temperature ** 2 / batch             # the customary weight of a softened loss
+    weight = torch.full((batch,), scale, device=device)
+    with torch.no_grad():
+        plain, kept = held_out(forms["bf16"](Xe))
+    for name, form in forms.items():
+        with torch.no_grad():
+            logits = form(Xe)
+            stat, r = held_out(logits)
+            far = L.token_logprobs(forms["bf16"](Xe), top=64)
+            stat["divergence"] = L.distill_loss(logits, far.top_id, far.top_logprob).mean().item()
+        stat["same_best"] = (r.top_id == kept.top_id).float().mean().item()
+        out["teacher"][name] = stat
+        student, opt = _token_mlp(64, 128, vocab, torch.Generator().manual_seed(seed + 1), device)
+        loss = None
+        for x, _ in batches():
+            with torch.no_grad():
+                a = L.token_logprobs(form(x), top=top, temperature=temperature)
+            logits = _logits(student, x)
+            loss, grad = L.distill_grad(logits.detach(), a.top_id, a.top_logprob, weight,
+                                        temperature=temperature)
+            logits.backward(grad)
+            opt.step()
+            opt.zero_grad()
+        with torch.no_grad():
+            stat, _ = held_out(_logits(student, Xe))
+        stat["divergence"] = loss.mean().item() if loss is not None else None
+        out["student"][name] = stat
+    return out
+
+
 def main() -> None:
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--n", type=int, default=1 << 22)
@@ -197,6 +288,7 @@ def main() -> None:
     a = ap.parse_args()
     r = run(a.n, a.seed)
     r["training"] = training_study()
+    r["distillation"] = distillation_study()
     text = json.dumps(r, indent=1)
     if a.out:
         with open(a.out, "w") as f:
