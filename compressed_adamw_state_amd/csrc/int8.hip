@@ -83,10 +83,10 @@ __device__ __forceinline__ void word_codes(const u32x4& v, int64_t j, int64_t co
 template <int kType, int kWaves, int kVecs>
 __global__ __launch_bounds__(kWaves * kWave) void quantize_rows_kernel(
     const typename Elem<kType>::T* x, int64_t cols, int64_t stride, int64_t ld, int8_t* codes,
-    float* scale) {
+    float* scale, int64_t first) {
     constexpr int E = Elem<kType>::kE;
     __shared__ uint32_t red[kWaves];
-    const int64_t row = blockIdx.x;
+    const int64_t row = first + blockIdx.x;
     const typename Elem<kType>::T* p = x + row * stride;
     u32x4 r[kVecs];
     uint32_t top = 0;
@@ -110,10 +110,10 @@ template <int kType>
 __global__ __launch_bounds__(kBlock) void quantize_long_kernel(const typename Elem<kType>::T* x,
                                                                int64_t cols, int64_t stride,
                                                                int64_t ld, int8_t* codes,
-                                                               float* scale) {
+                                                               float* scale, int64_t first) {
     constexpr int E = Elem<kType>::kE;
     __shared__ uint32_t red[kWavesPerBlock];
-    const int64_t row = blockIdx.x;
+    const int64_t row = first + blockIdx.x;
     const typename Elem<kType>::T* p = x + row * stride;
     uint32_t top = 0;
     for (int64_t w = threadIdx.x; w * E < cols; w += kBlock) {
@@ -132,8 +132,8 @@ __global__ __launch_bounds__(kBlock) void quantize_long_kernel(const typename El
 template <int kOpt, bool kFp32>
 __global__ __launch_bounds__(kBlock) void quantize_state_kernel(DevTensor d, int64_t cols,
                                                                 int64_t ld, int8_t* codes,
-                                                                float* scale) {
-    const int64_t row = blockIdx.x;
+                                                                float* scale, int64_t first) {
+    const int64_t row = first + blockIdx.x;
     const GTensor T = view(d);
     auto load = [&](int64_t j) -> float {
         const int64_t e = row * cols + j;
@@ -671,10 +671,23 @@ static int check_matrix(int64_t rows, int64_t cols) {
     return FLASHOPT_OK;
 }
 
+// the product's tiles are counted in 32 bits
+static int check_outputs(int64_t m, int64_t n) {
+    return (m / 128 + 1) * (n / 128 + 1) > (int64_t(1) << 30) ? FLASHOPT_ERR_SIZE : FLASHOPT_OK;
+}
+
 static int check_codes(const void* codes, const void* scale) {
     if (!codes || !scale) return FLASHOPT_ERR_NULL;
     if (!aligned(codes, 16) || !aligned(scale, 4)) return FLASHOPT_ERR_ALIGN;
     return FLASHOPT_OK;
+}
+
+// A launch has less than 2^32 threads: rows in parts of 2^21 blocks.
+template <typename F>
+static void by_rows(int64_t rows, F f) {
+    constexpr int64_t kPart = int64_t(1) << 21;
+    for (int64_t first = 0; first < rows; first += kPart)
+        f(first, dim3((unsigned)(rows - first < kPart ? rows - first : kPart)));
 }
 
 static int launch_quantize(const void* x, int32_t type, int64_t rows, int64_t cols, int64_t stride,
@@ -683,16 +696,21 @@ static int launch_quantize(const void* x, int32_t type, int64_t rows, int64_t co
     return by_type(type, [&](auto k) {
         constexpr int kType = decltype(k)::value, E = Elem<kType>::kE;
         const auto* p = (const typename Elem<kType>::T*)x;
-        const dim3 grid((unsigned)rows);
-        // the fewest waves and words that hold a row
-        if (ld <= 2 * kWave * E)
-            hipLaunchKernelGGL((quantize_rows_kernel<kType, 1, 2>), grid, dim3(kWave), 0, st, p, cols, stride, ld, codes, scale);
-        else if (ld <= 2 * kBlock * E)
-            hipLaunchKernelGGL((quantize_rows_kernel<kType, 4, 2>), grid, dim3(kBlock), 0, st, p, cols, stride, ld, codes, scale);
-        else if (ld <= 8 * kBlock * E)
-            hipLaunchKernelGGL((quantize_rows_kernel<kType, 16, 2>), grid, dim3(16 * kWave), 0, st, p, cols, stride, ld, codes, scale);
-        else
-            hipLaunchKernelGGL((quantize_long_kernel<kType>), grid, dim3(kBlock), 0, st, p, cols, stride, ld, codes, scale);
+        by_rows(rows, [&](int64_t first, dim3 grid) {
+            // the fewest waves and words that hold a row
+            if (ld <= 2 * kWave * E)
+                hipLaunchKernelGGL((quantize_rows_kernel<kType, 1, 2>), grid, dim3(kWave), 0, st, p,
+                                   cols, stride, ld, codes, scale, first);
+            else if (ld <= 2 * kBlock * E)
+                hipLaunchKernelGGL((quantize_rows_kernel<kType, 4, 2>), grid, dim3(kBlock), 0, st, p,
+                                   cols, stride, ld, codes, scale, first);
+            else if (ld <= 8 * kBlock * E)
+                hipLaunchKernelGGL((quantize_rows_kernel<kType, 16, 2>), grid, dim3(16 * kWave), 0, st,
+                                   p, cols, stride, ld, codes, scale, first);
+            else
+                hipLaunchKernelGGL((quantize_long_kernel<kType>), grid, dim3(kBlock), 0, st, p, cols,
+                                   stride, ld, codes, scale, first);
+        });
     });
 }
 
@@ -727,6 +745,7 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k) {
     // again for every 16 channels count, but tiles need channels to fill the
     // GPU: 32 tokens, 14336 x 4096: 27.7 us here, 24.6 in tiles; 4096 x 14336: 26
     // and, even split, 34.
+    // (64 tokens of 4096 x 4096: 16 us, 22 in tiles)
     p.skinny = m <= 16 ? 1 : m <= 32 && tn < 96 ? 2 : m <= 64 && tn < 96 ? 4 : 0;
     if (p.skinny) return p;
     // 4096 x 4096 x 4096 in large tiles: 64 us; 2048 x 4096 x 4096 in small ones 40
@@ -838,28 +857,29 @@ int flashopt_tensor_quantize_rows(const flashopt_tensor* t, int32_t kind, int64_
     const int c = check_codes(codes, scale);
     if (c) return c;
     const DevTensor d = to_dev(*t);
-    const dim3 grid((unsigned)rows);
     const int64_t ld = ld_of(cols);
     hipStream_t st = (hipStream_t)stream;
-    const bool adam = opt_of(kind) == kAdamW;     // SGD and Lion share a layout
-    if (is_fp32(kind)) {
-        if (adam) hipLaunchKernelGGL((quantize_state_kernel<kAdamW, true>), grid, dim3(kBlock), 0, st, d, cols, ld, codes, scale);
-        else hipLaunchKernelGGL((quantize_state_kernel<kSgd, true>), grid, dim3(kBlock), 0, st, d, cols, ld, codes, scale);
-    } else {
-        if (adam) hipLaunchKernelGGL((quantize_state_kernel<kAdamW, false>), grid, dim3(kBlock), 0, st, d, cols, ld, codes, scale);
-        else hipLaunchKernelGGL((quantize_state_kernel<kSgd, false>), grid, dim3(kBlock), 0, st, d, cols, ld, codes, scale);
-    }
+    const bool adam = opt_of(kind) == kAdamW, fp32 = is_fp32(kind);      // SGD and Lion share a layout
+    by_rows(rows, [&](int64_t first, dim3 grid) {
+        auto launch = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, grid, dim3(kBlock), 0, st, d, cols, ld, codes, scale, first);
+        };
+        if (fp32 && adam) launch(quantize_state_kernel<kAdamW, true>);
+        else if (fp32) launch(quantize_state_kernel<kSgd, true>);
+        else if (adam) launch(quantize_state_kernel<kAdamW, false>);
+        else launch(quantize_state_kernel<kSgd, false>);
+    });
     return launch_status();
 }
 
 size_t flashopt_int8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-    if (check_matrix(m, k) || check_matrix(n, k) || m == 0 || n == 0 || few_tokens(m, n, k)) return 0;
+    if (check_matrix(m, k) || check_matrix(n, k) || check_outputs(m, n) || m == 0 || n == 0 || few_tokens(m, n, k)) return 0;
     return up256(plan_of(m, n, k).sums) + up256((size_t)(m * ld_of(k))) +
            up256((size_t)m * sizeof(float));
 }
 
 size_t flashopt_int8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-    if (check_matrix(m, k) || check_matrix(n, k) || m == 0 || n == 0) return 0;
+    if (check_matrix(m, k) || check_matrix(n, k) || check_outputs(m, n) || m == 0 || n == 0) return 0;
     return plan_of(m, n, k).sums;
 }
 
@@ -879,7 +899,7 @@ int flashopt_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b,
                          void* out, int32_t out_type, int64_t out_stride, void* workspace,
                          size_t workspace_bytes, void* stream) {
     if (!valid_type(out_type)) return FLASHOPT_ERR_ARG;
-    if (check_matrix(m, k) || check_matrix(n, k) || out_stride < n || out_stride > kMaxNumel)
+    if (check_matrix(m, k) || check_matrix(n, k) || check_outputs(m, n) || out_stride < n || out_stride > kMaxNumel)
         return FLASHOPT_ERR_SIZE;
     if (m == 0 || n == 0) return FLASHOPT_OK;
     const int e = check_product(a, a_scale, b, b_scale, bias, out, out_type);
@@ -898,7 +918,7 @@ int flashopt_int8_linear(const void* x, int32_t type, int64_t m, int64_t k, int6
                          void* out, int64_t out_stride, void* workspace, size_t workspace_bytes,
                          void* stream) {
     if (!valid_type(type)) return FLASHOPT_ERR_ARG;
-    if (check_matrix(m, k) || check_matrix(n, k) || out_stride < n || out_stride > kMaxNumel ||
+    if (check_matrix(m, k) || check_matrix(n, k) || check_outputs(m, n) || out_stride < n || out_stride > kMaxNumel ||
         x_stride < k || x_stride > kMaxNumel)
         return FLASHOPT_ERR_SIZE;
     if (m == 0 || n == 0) return FLASHOPT_OK;

@@ -3,21 +3,23 @@
 // logits, and their gradients.
 //
 // Mathematics.  With c = log2(e) / T and any shift m, a row's distribution is
-// p_j = 2^((x_j - m) c) / S, S = sum_j 2^((x_j - m) c).  Each work item (a
-// block, over one chunk of one row held in registers) forms the chunk's own
-// maximum m and sums
+// p_j = 2^((x_j - m) c) / S, S = sum_j 2^((x_j - m) c).  A thread sums, over its
+// words of a segment of a row, with a shift of its own,
 //   S = sum_j e_j,  U = sum_j e_j d_j   (d_j = (x_j - m) c, e_j = 2^d_j);
-// a join over the row's chunks rescales them to the row's maximum:
-//   S = sum S_c 2^(D_c),  U = sum 2^(D_c) (U_c + D_c S_c),  D_c = (m_c - m) c.
+// joining threads, waves and segments rescales them to one shift:
+//   S = sum S_k 2^(D_k),  U = sum 2^(D_k) (U_k + D_k S_k),  D_k = (m_k - m) c.
 // Then log2 p_j = d_j - log2 S and H = ln2 (log2 S - U / S), both without
-// cancellation.  The difference x - m is formed before the scaling, so that
-// entries of the type's lowest value stay finite and a row of nothing else is
-// uniform.
+// cancellation.
 //
 // The gradients are elementwise in the row's numbers: one more pass over the
-// chunks, plus a few entries (the given token, the teacher's alternatives)
-// that the chunk's block writes again after its dense pass, from logits it
-// read before it, so that a gradient may replace its logits.
+// words, plus a few entries (the given token, the teacher's alternatives) that
+// the block writes again after its dense pass, from logits it read before it, so
+// that a gradient may replace its logits.
+//
+// Rows of BF16 bring 8.5 issue slots an entry (unpack, maximum of two, fma, exp2
+// at a quarter of the rate, two sums) for 2 bytes: 65 us at 2048 x 128256 where
+// HBM takes 97, so the forward pass is bound by HBM (2048 x 128256 BF16: 97 us,
+// 5.4 TB/s; with the 64 best entries 124).
 #include <cmath>
 
 #include "logits.hpp"
@@ -53,7 +55,6 @@ __device__ __forceinline__ void write_top(const ProbOut& o, int64_t row, int top
     o.top_id[row * top + k] = entry_id(e);
     o.top_logprob[row * top + k] = ((key_value(entry_key(e)) - st.m) * c - st.l2s) * kLn2;
 }
-
 
 // A segment of a row: the words [begin, end) of 16 bytes; the row's last
 // word may be partial.  Chunks are kVecs words of each of kThreads threads.
@@ -789,41 +790,6 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(RowsIn<kType> in, 
 
 // ---- host ---------------------------------------------------------------------
 
-static int check_rows(const void* logits, int32_t type, int64_t rows, int64_t vocab, int64_t stride,
-                      double temperature) {
-    if (!valid_type(type)) return FLASHOPT_ERR_ARG;
-    if (rows < 0 || vocab < 1 || vocab > FLASHOPT_VOCAB_MAX || stride < vocab ||
-        stride > kMaxNumel || rows > INT32_MAX / ((vocab + 4095) / 4096))
-        return FLASHOPT_ERR_SIZE;
-    // 1/T and log2(e)/T are used as normal binary32 numbers
-    if (!(temperature >= 0x1p-126) || !(temperature <= 0x1p126)) return FLASHOPT_ERR_ARG;
-    if (rows == 0) return FLASHOPT_OK;
-    if (!logits) return FLASHOPT_ERR_NULL;
-    if (!aligned(logits, type_size(type))) return FLASHOPT_ERR_ALIGN;
-    return FLASHOPT_OK;
-}
-
-static int check_grad(const void* grad, int32_t type, int64_t vocab, int64_t grad_stride) {
-    if (!grad) return FLASHOPT_ERR_NULL;
-    if (grad_stride < vocab || grad_stride > kMaxNumel) return FLASHOPT_ERR_SIZE;
-    if (!aligned(grad, type_size(type))) return FLASHOPT_ERR_ALIGN;
-    return FLASHOPT_OK;
-}
-
-static int check_workspace(const void* workspace, size_t have, size_t need) {
-    if (need == 0) return FLASHOPT_OK;
-    if (!workspace) return FLASHOPT_ERR_NULL;
-    if (have < need || !aligned(workspace, 256)) return FLASHOPT_ERR_WORKSPACE;
-    return FLASHOPT_OK;
-}
-
-static int check_list(const int64_t* top_id, const float* top_logprob, int32_t top, int64_t vocab) {
-    if (top < 1 || top > FLASHOPT_TOP_MAX || top > vocab) return FLASHOPT_ERR_ARG;
-    if (!top_id || !top_logprob) return FLASHOPT_ERR_NULL;
-    if (!aligned(top_id, 8) || !aligned(top_logprob, 4)) return FLASHOPT_ERR_ALIGN;
-    return FLASHOPT_OK;
-}
-
 // How a call cuts its rows.  A block streams a segment of a row.  From
 // kBlocksWanted rows on (a block for each CU) a segment is the whole row: no
 // join, one launch.  With fewer the rows are cut until that many blocks run (at
@@ -855,11 +821,55 @@ static Cut cut_rows(int32_t type, int64_t rows, int64_t vocab) {
     return k;
 }
 
+// a launch has less than 2^32 threads
+static bool rows_fit(int32_t type, int64_t rows, int64_t vocab) {
+    return rows <= FLASHOPT_ROWS_MAX && rows * cut_rows(type, rows, vocab).nseg <= FLASHOPT_ROWS_MAX;
+}
+
+static int check_rows(const void* logits, int32_t type, int64_t rows, int64_t vocab, int64_t stride,
+                      double temperature) {
+    if (!valid_type(type)) return FLASHOPT_ERR_ARG;
+    if (rows < 0 || vocab < 1 || vocab > FLASHOPT_VOCAB_MAX || stride < vocab ||
+        stride > kMaxNumel || !rows_fit(type, rows, vocab))
+        return FLASHOPT_ERR_SIZE;
+    // 1/T and log2(e)/T are used as normal binary32 numbers
+    if (!(temperature >= 0x1p-126) || !(temperature <= 0x1p126)) return FLASHOPT_ERR_ARG;
+    if (rows == 0) return FLASHOPT_OK;
+    if (!logits) return FLASHOPT_ERR_NULL;
+    if (!aligned(logits, type_size(type))) return FLASHOPT_ERR_ALIGN;
+    return FLASHOPT_OK;
+}
+
+static int check_grad(const void* grad, int32_t type, int64_t vocab, int64_t grad_stride) {
+    if (!grad) return FLASHOPT_ERR_NULL;
+    if (grad_stride < vocab || grad_stride > kMaxNumel) return FLASHOPT_ERR_SIZE;
+    if (!aligned(grad, type_size(type))) return FLASHOPT_ERR_ALIGN;
+    return FLASHOPT_OK;
+}
+
+static int check_workspace(const void* workspace, size_t have, size_t need) {
+    if (need == 0) return FLASHOPT_OK;
+    if (!workspace) return FLASHOPT_ERR_NULL;
+    if (have < need || !aligned(workspace, 256)) return FLASHOPT_ERR_WORKSPACE;
+    return FLASHOPT_OK;
+}
+
+static int check_list(const int64_t* top_id, const float* top_logprob, int32_t top, int64_t vocab) {
+    if (top < 1 || top > FLASHOPT_TOP_MAX || top > vocab) return FLASHOPT_ERR_ARG;
+    if (!top_id || !top_logprob) return FLASHOPT_ERR_NULL;
+    if (!aligned(top_id, 8) || !aligned(top_logprob, 4)) return FLASHOPT_ERR_ALIGN;
+    return FLASHOPT_OK;
+}
+
 // a row that one block holds needs no workspace
 static size_t parts_bytes(const Cut& k, int64_t rows) {
     if (k.nseg == 1) return 0;
     const size_t b = (size_t)(rows * k.nseg) * sizeof(Part);
     return (b + 255) & ~size_t(255);
+}
+// and, for the gradient in the same call, stats behind the parts
+static size_t both_bytes(const Cut& k, int64_t rows) {
+    return k.nseg == 1 ? 0 : parts_bytes(k, rows) + (size_t)rows * sizeof(DistillStats);
 }
 
 // f is called with the type and the chunk's words as compile-time constants
@@ -960,7 +970,18 @@ static int launch_prob_both(const Rows& a, const ProbOut& out, void* workspace, 
                                out, 0, part, nullptr, G);
     });
     if (f || k.nseg == 1) return f;
-    return launch_prob_grad(a, k, out, part, nullptr, g, st);
+    if (g.grad != a.logits) return launch_prob_grad(a, k, out, part, nullptr, g, st);
+    // A gradient in the logits' place: a segment's block would replace the given
+    // token's logit before the row's first block has read it.  So the row is
+    // finished by a launch of its own.
+    ProbOut first = out, none = {out.targets, nullptr, nullptr, nullptr, nullptr, nullptr};
+    first.stats = (ProbStats*)((char*)workspace + parts_bytes(k, a.rows));
+    by_type(a.type, k.vecs, [&](auto t, auto) {
+        constexpr int kType = decltype(t)::value;
+        hipLaunchKernelGGL((prob_join_kernel<kType>), dim3((unsigned)a.rows), dim3(kBlock), 0, st,
+                           rows_in<kType>(a, k), first, 0, part, nullptr);
+    });
+    return launch_prob_grad(a, k, none, nullptr, (const float*)first.stats, g, st);
 }
 
 static int launch_distill_grad(const Rows& a, const Cut& k, const DistillIn& list,
@@ -991,11 +1012,15 @@ static int launch_distill(const Rows& a, const DistillIn& list, void* workspace,
         else
             hipLaunchKernelGGL((distill_kernel<kType, kVecs, false>), grid, dim3(kBlock), lds, st, in,
                                list, part, loss, (DistillStats*)stats, G);
-        if (k.nseg > 1 && !g.grad)
+        // (a gradient in the logits' place: as in launch_prob_both)
+        if (k.nseg > 1 && (!g.grad || g.grad == a.logits)) {
+            if (g.grad) stats = (float*)((char*)workspace + parts_bytes(k, a.rows));
             hipLaunchKernelGGL((distill_join_kernel<kType>), dim3((unsigned)a.rows), dim3(kWave), 0,
                                st, in, list, part, loss, (DistillStats*)stats);
+        }
     });
     if (f || k.nseg == 1 || !g.grad) return f;
+    if (g.grad == a.logits) return launch_distill_grad(a, k, list, nullptr, nullptr, stats, g, st);
     return launch_distill_grad(a, k, list, part, loss, nullptr, g, st);
 }
 
@@ -1007,11 +1032,12 @@ extern "C" {
 
 size_t flashopt_logprob_workspace_bytes(int32_t type, int64_t rows, int64_t vocab, int32_t top) {
     if (!valid_type(type) || rows < 0 || vocab < 1 || vocab > FLASHOPT_VOCAB_MAX || top < 0 ||
-        top > FLASHOPT_TOP_MAX || rows > INT32_MAX / ((vocab + 4095) / 4096))
+        top > FLASHOPT_TOP_MAX || !rows_fit(type, rows, vocab))
         return 0;
     const Cut k = cut_rows(type, rows, vocab);
     if (k.nseg == 1) return 0;
-    return parts_bytes(k, rows) + (size_t)(rows * k.nseg) * (size_t)top * sizeof(uint64_t);
+    const size_t forward = parts_bytes(k, rows) + (size_t)(rows * k.nseg) * (size_t)top * sizeof(uint64_t);
+    return forward > both_bytes(k, rows) ? forward : both_bytes(k, rows);
 }
 
 int flashopt_logprob(const void* logits, int32_t type, int64_t rows, int64_t vocab,

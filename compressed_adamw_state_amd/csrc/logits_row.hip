@@ -190,13 +190,18 @@ static bool by_row(const Rows& a, F f) {
     if (words > (int64_t)waves * kWave * 16) return false;
     const int cols = (int)((words + waves * kWave - 1) / (waves * kWave));
     auto with = [&](auto t) {
-        auto by_cols = [&](auto w) {
-            if (cols <= 8) f(t, w, std::integral_constant<int, 8>());
-            else if (cols <= 12) f(t, w, std::integral_constant<int, 12>());
-            else f(t, w, std::integral_constant<int, 16>());
-        };
-        if (waves == 4) by_cols(std::integral_constant<int, 4>());
-        else by_cols(std::integral_constant<int, 8>());
+        const std::integral_constant<int, 4> w4;
+        const std::integral_constant<int, 8> w8;
+        const std::integral_constant<int, 12> c12;
+        const std::integral_constant<int, 16> c16;
+        if (waves == 4) {
+            if (cols <= 8) f(t, w4, std::integral_constant<int, 8>());
+            else if (cols <= 12) f(t, w4, c12);
+            else f(t, w4, c16);
+        } else {                                 // more than half of 16 columns
+            if (cols <= 12) f(t, w8, c12);
+            else f(t, w8, c16);
+        }
     };
     if (a.type == FLASHOPT_BF16) with(std::integral_constant<int, FLASHOPT_BF16>());
     else if (a.type == FLASHOPT_FP16) with(std::integral_constant<int, FLASHOPT_FP16>());

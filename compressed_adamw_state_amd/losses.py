@@ -158,6 +158,8 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
 def _grad_buffer(logits: torch.Tensor, inplace: bool):
     """(the gradient, its row stride)"""
     if inplace:
+        # torch then refuses a backward pass that would read the logits' values
+        torch.autograd.graph.increment_version(logits)
         return logits.detach(), F.row_stride(_rows(logits))
     return _empty(logits.shape, logits.device, logits.dtype), logits.shape[-1]
 

@@ -45,11 +45,13 @@ typedef enum flashopt_type {
  * its row's log probability is 0 and has no gradient, and a teacher's
  * alternative with such an id is skipped.  Ids are never read out of range.
  *
- * Limits: 0 <= rows, rows * ceil(vocab / 4096) < 2^31, 1 <= vocab <=
- * FLASHOPT_VOCAB_MAX, 0 <= top <= FLASHOPT_TOP_MAX and top <= vocab.
+ * Limits: 0 <= rows <= FLASHOPT_ROWS_MAX (a quarter of that above a vocabulary of
+ * 131072), 1 <= vocab <= FLASHOPT_VOCAB_MAX, 0 <= top <= FLASHOPT_TOP_MAX and
+ * top <= vocab.
  * Errors: FLASHOPT_ERR_SIZE, FLASHOPT_ERR_NULL, FLASHOPT_ERR_ARG (type,
  * temperature, top), FLASHOPT_ERR_ALIGN (a pointer not aligned to its element
  * type; workspace 256 bytes), FLASHOPT_ERR_WORKSPACE, FLASHOPT_ERR_HIP. */
+#define FLASHOPT_ROWS_MAX 8388608
 #define FLASHOPT_VOCAB_MAX 524288
 #define FLASHOPT_TOP_MAX 64
 
@@ -124,8 +126,8 @@ int flashopt_distill_grad(const void* logits, int32_t type, int64_t rows, int64_
  * the quotient decided as if exact; a row of zeros has codes and scale 0.  A
  * row holding an infinity or NaN has codes 0 and scale NaN, so that all that
  * is computed from it is NaN.  Codes are 16-byte aligned, scales 4.
- * Limits: rows <= 2^24 (products), cols <= FLASHOPT_INT8_COLS_MAX (so that a sum of
- * products fits a 32-bit integer). */
+ * Limits: rows <= 2^24, cols <= FLASHOPT_INT8_COLS_MAX (so that a sum of products
+ * fits a 32-bit integer); a product m n <= 2^44. */
 #define FLASHOPT_INT8_COLS_MAX 131072
 int64_t flashopt_int8_ld(int64_t cols);
 /* From rows x cols values of `type`, row stride `stride` elements. */

@@ -1,4 +1,4 @@
-"""Plain 64-bit forms of the language-model operators, on the CPU, with the
+"""Plain 64-bit forms of the language-model operators, in torch, with the
 error each binary32 result of the library may have.
 
 The bounds count roundings of u = 2^-24 (a binary32 operation; the hardware
@@ -6,12 +6,15 @@ exp2 and log2 2u).  With d = z_j - max z: an exponential e^d is off by
 (3 |d| + 2) u relatively (difference, factor, product, exp2); a sum of
 positive terms by at most 100 u more (at most 64 + 8 additions per thread, a
 tree, a join of chunks).  A mean of terms over p is bounded with the means of
-|d| and d^2 under p.  Results in 16 bits add half a step of their type."""
+|d| and d^2 under p.  Results in 16 bits add half a step of their type.  The
+hardware exp2 gives 0 below 2^-126 (TINY), so a gradient, an exponential times a
+factor, may also be off by TINY times that factor."""
 import math
 
 import torch
 
 U = 2.0 ** -24
+TINY = 2.0 ** -126
 
 
 def half_step(t: torch.dtype) -> float:
@@ -67,20 +70,21 @@ def logprob_grad(x, targets, gl, gh, temperature):
     d, logp, p, m1, m2, empty = dist(x, temperature)
     vocab, rows = x.shape[1], x.shape[0]
     given = (targets >= 0) & (targets < vocab) & ~empty
-    gl = torch.where(given, gl.double(), 0.0) if gl is not None else torch.zeros(rows).double()
-    gh = gh.double() if gh is not None else torch.zeros(rows).double()
+    gl = torch.where(given, gl.double(), 0.0) if gl is not None else torch.zeros(rows, device=x.device).double()
+    gh = gh.double() if gh is not None else torch.zeros(rows, device=x.device).double()
     lpf = torch.where(p > 0, logp, 0.0)
     ent = -(p * lpf).sum(1)
     a = (-gl - gh * ent)[:, None]
     grad = p * (a - gh[:, None] * lpf)
-    grad[torch.arange(rows)[given], targets[given]] += gl[given]
+    grad[torch.arange(rows, device=x.device)[given], targets[given]] += gl[given]
     # p's relative error, and the absolute one of the factor (H and log p)
     df = torch.where(p > 0, d, 0.0).abs()
     rel = lse_tol(m1)[:, None] + U * (4 * df + 8)
     factor = gl.abs()[:, None] + gh.abs()[:, None] * (ent[:, None] + lpf.abs())
     ftol = gh.abs()[:, None] * (lse_tol(m1) + U * (3 * m2 + 210 * m1 + 8 * ent))[:, None] \
         + gh.abs()[:, None] * rel + 6 * U * factor
-    tol = p * (rel * factor + ftol) + 4 * U * grad.abs()
+    lost = TINY * (gl.abs() + gh.abs() * (ent + 90))[:, None]                # |log p| <= 88 there
+    tol = p * (rel * factor + ftol) + 4 * U * grad.abs() + lost
     return grad / temperature, tol / temperature
 
 
@@ -97,13 +101,12 @@ def distill(x, ids, t, tail, temperature, g=None):
     q = torch.exp(td)
     on = ok.any(1) & ~empty
     lp = logp.gather(1, at)
-    listed = torch.zeros(rows, vocab, dtype=torch.bool)
-    for r in range(rows):
-        listed[r, ids[r][ok[r]]] = True
+    listed = torch.zeros(rows, vocab, dtype=torch.bool, device=x.device)
+    listed[torch.arange(rows, device=x.device)[:, None].expand_as(ids)[ok], ids[ok]] = True
     P = torch.where(listed, 0.0, p).sum(1)
     rest_lse = torch.logsumexp(torch.where(listed, -math.inf, logp), 1)     # log P, also where P underflows
     Q = q.sum(1)
-    r = (1.0 - Q).clamp_min(0.0) if tail else torch.zeros(rows).double()
+    r = (1.0 - Q).clamp_min(0.0) if tail else torch.zeros(rows, device=x.device).double()
     has_rest = rest_lse > -math.inf
     r = torch.where(has_rest, r, 0.0)
     terms = torch.where(q > 0, q * (td - lp), 0.0)
@@ -127,15 +130,15 @@ def distill(x, ids, t, tail, temperature, g=None):
     # the entries' shares of the rest, from the rest's own largest (far below 1 where P underflows)
     rest = torch.where(listed, -math.inf, x.double() / temperature)
     share = torch.where(has_rest[:, None], torch.softmax(rest, 1), 0.0)
-    qsum = torch.zeros(rows, vocab, dtype=torch.float64)
+    qsum = torch.zeros(rows, vocab, dtype=torch.float64, device=x.device)
     qsum.scatter_add_(1, at, torch.where(ok, q, 0.0))
     grad = w * (qr * p - qsum - r[:, None] * share)
     df = torch.where(p > 0, d, 0.0).abs()
     rel = 2 * lse_tol(m1)[:, None] + U * (8 * df + 130)
-    qst = torch.zeros(rows, vocab, dtype=torch.float64)
+    qst = torch.zeros(rows, vocab, dtype=torch.float64, device=x.device)
     qst.scatter_add_(1, at, torch.where(ok, qtol, 0.0))
     gtol = w.abs() * (qr * p * rel + qst + 70 * U * qsum + share * ((rtol * 2 + 4 * U)[:, None]
-                      + (r[:, None] + qr * P[:, None]) * rel)) + 4 * U * grad.abs()
+                      + (r[:, None] + qr * P[:, None]) * rel) + TINY * (2 * qr + r[:, None])) + 4 * U * grad.abs()
     return loss, tol, grad / temperature, gtol / temperature
 
 

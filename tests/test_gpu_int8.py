@@ -70,6 +70,8 @@ def test_quantize_borders_and_special_rows(dtype):
 
 
 SHAPES = [(1, 1, 1), (1, 64, 128), (1, 4099, 4096), (1, 33, 33001), (2, 130, 77), (2, 40, 9000), (3, 1000, 4097), (5, 31, 1300),
+          # tiles of 256 x 256 (more than blocks in the last), small tiles more than blocks
+          (2600, 5200, 384), (8000, 1700, 129), (5000, 6001, 300), (3300, 3299, 130), (3300, 3300, 640),
           (7, 257, 768), (8, 70, 2050), (8, 50, 5000), (9, 100, 640), (16, 50257, 768),
           (17, 100, 300), (33, 513, 1024), (63, 640, 129), (65, 2304, 768), (100, 129, 2048), (129, 257, 640), (200, 1000, 5120),
           (256, 256, 256), (300, 700, 14336), (70, 1, 2048), (129, 130, 2176), (66, 4000, 3456), (513, 1025, 384), (1000, 2304, 768), (2049, 300, 130)]

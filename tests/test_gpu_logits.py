@@ -15,7 +15,7 @@ from compressed_adamw_state_amd import losses as L
 pytestmark = pytest.mark.gpu
 
 TYPES = [torch.bfloat16, torch.float16, torch.float32]
-VOCABS = [1, 2, 7, 8, 9, 64, 65, 1000, 4095, 8191, 8193, 16383, 16385, 50257, 131073]
+VOCABS = [1, 2, 7, 8, 9, 64, 65, 1000, 4095, 8191, 8193, 16383, 16385, 50257, 131073, 300001]
 
 
 def near(got, ref, tol, dtype=torch.float32):
@@ -223,7 +223,6 @@ def test_distill_odd_lists(dtype, tail):
     ids[0, 7] = ids[0, 1]
     ids[1, 0], ids[1, 5] = -100, vocab
     ids[2, :] = -1
-    x[3] -= 0.0
     x[3, ids[3]] = -30.0                                   # the student finds them unlikely
     x[4] = -30.0
     x[4, ids[4]] = 30.0                                    # the student finds nothing else likely
@@ -267,6 +266,73 @@ def test_gradients_against_differences():
         assert (diff - grad[0]).abs().max().item() < 1.1e-3
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", [4101, 8193, 8203, 12301, 16387, 24580, 32768, 32771, 40000, 50257, 65536, 65543])
+def test_rows_of_one_block(dtype, vocab):
+    """256 rows and more: each held or streamed by one block (more rows than blocks at once for the
+    small vocabularies), with rows that need the exceptional paths."""
+    rows = 1100 if vocab < 16000 else 300
+    x, t, g = draw(rows, vocab, dtype, vocab)
+    x[3] = -math.inf                                       # nothing left
+    x[4, :vocab - 2] = -math.inf                           # the row's last entries only
+    x[5] = torch.finfo(dtype).min                          # the lowest value everywhere
+    x[6, vocab // 2] = 300.0                               # far above what comes first
+    x[7, vocab - 1] = 60000.0                              # the last entry far above all
+    x[8, ::3] = -math.inf
+    x[9] = x[9].sort()[0]                                  # rising
+    x[10] = -math.inf
+    x[10, 1] = -2.0
+    x[11] *= 1000                                          # large magnitudes
+    t[4], t[7], t[10] = vocab - 1, vocab - 1, 1
+    gl, gh = torch.randn(rows, generator=g), torch.randn(rows, generator=g)
+    xc, tc, glc, ghc = x.cuda(), t.cuda(), gl.cuda(), gh.cuda()
+    for temp, b in ((1.0, None), (0.7, ghc)):
+        r = L.token_logprobs_grad(xc, tc, glc, b, temperature=temp)
+        ref, tol = P.logprob_grad(xc, tc, glc, b, temp)
+        near(r.grad, ref, tol, dtype)
+        lp, lt, en, et = P.logprob(xc, tc, temp)
+        near(r.logprob, lp, lt)
+        near(r.entropy, en, et)
+        wide = place(x, "strided")
+        two = L.token_logprobs_grad(wide, tc, glc, b, temperature=temp, inplace=True)
+        near(wide, ref, tol, dtype)
+        assert torch.equal(two.logprob, r.logprob)
+        del ref, tol
+    r = L.token_logprobs(xc, tc, top=20)
+    near(r.logprob, *P.logprob(xc, tc, 1.0)[:2])
+    assert torch.equal(r.top_id, P.top(xc, 20))
+    xc[13, 5], xc[14, vocab - 1] = math.nan, math.inf      # and nothing but those rows is lost
+    r = L.token_logprobs_grad(xc, tc, glc)
+    bad = torch.isnan(r.grad).any(1)
+    assert bad.nonzero().flatten().tolist() == [13, 14] and torch.isnan(r.entropy[[13, 14]]).all()
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", [1003, 16385, 50257, 131075])
+def test_distill_rows_of_one_block(dtype, vocab, tail):
+    rows = 260
+    x, _, g = draw(rows, vocab, dtype, vocab + 1)
+    x[3] = -math.inf
+    x[5] = torch.finfo(dtype).min
+    x[6, vocab // 2] = 300.0
+    x[11] *= 100
+    xc = x.cuda()
+    z = xc.double() + torch.randn(rows, vocab, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+    z[3] = 0.0
+    v, ids = torch.topk(z, 30, dim=1)
+    tlp = (v - torch.logsumexp(z, 1, keepdim=True)).float()
+    up = torch.randn(rows, generator=g).cuda()
+    a, at, b, bt = P.distill(xc, ids, tlp, tail, 1.0, up)
+    loss, grad = L.distill_grad(xc, ids, tlp, up, tail=tail)
+    near(loss, a, at)
+    near(grad, b, bt, dtype)
+    wide = place(x, "strided")
+    loss2, _ = L.distill_grad(wide, ids, tlp, up, tail=tail, inplace=True)
+    near(wide, b, bt, dtype)
+    assert torch.equal(loss, loss2)
+
+
 def test_many_rows_and_shapes():
     """More rows than the GPU holds blocks at once; leading dimensions; no rows."""
     x, t, g = draw(3000, 1003, torch.bfloat16, 9)
@@ -307,6 +373,35 @@ def test_other_stream_and_repeat():
     torch.cuda.synchronize()
     for a, b in zip(first, second):
         assert torch.equal(a, b)
+
+
+def test_gradient_in_the_logits_place_of_cut_rows():
+    """Few rows, each cut into many segments whose blocks replace their logits: the listed and given
+    entries of other segments must have been read before.  Equal to the gradient written elsewhere."""
+    for rows, vocab in ((1, 131072), (2, 100003), (5, 200000)):
+        x, t, g = draw(rows, vocab, torch.bfloat16, vocab)
+        ids, tlp = (v.cuda() for v in teacher(x, 64, 1.0, 3))
+        up = torch.randn(rows, generator=g).cuda()
+        for _ in range(5):
+            a, b = x.cuda(), x.cuda()
+            loss, grad = L.distill_grad(a, ids, tlp, up)
+            loss2, _ = L.distill_grad(b, ids, tlp, up, inplace=True)
+            assert torch.equal(loss, loss2) and torch.equal(grad, b)
+            b = x.cuda()
+            r = L.token_logprobs_grad(a, t.cuda(), up, up)
+            r2 = L.token_logprobs_grad(b, t.cuda(), up, up, inplace=True)
+            assert torch.equal(r.logprob, r2.logprob) and torch.equal(r.entropy, r2.entropy)
+            assert torch.equal(r.grad, b)
+
+
+def test_in_place_refuses_a_stale_backward():
+    """torch's graph sees that the logits' values are gone."""
+    x = torch.randn(4, 100, device="cuda", requires_grad=True)
+    y = x * 1.0
+    s = (y * y).sum()                                     # keeps y for its backward pass
+    L.token_logprobs_grad(y, torch.zeros(4, dtype=torch.int64, device="cuda"), torch.ones(4, device="cuda"), inplace=True)
+    with pytest.raises(RuntimeError):
+        s.backward()
 
 
 def test_captured_and_replayed():

@@ -26,7 +26,7 @@ def test_logprob_refusals():
     assert logprob(type=3) == -4 and logprob(type=-1) == -4
     assert logprob(rows=-1) == -2 and logprob(vocab=0) == -2 and logprob(vocab=524289, stride=524289) == -2
     assert logprob(stride=99) == -2 and logprob(rows=1 << 31) == -2 and logprob(stride=1 << 61) == -2
-    assert logprob(rows=1 << 27, vocab=100000, stride=100000) == -2
+    assert logprob(rows=(1 << 23) + 1) == -2 and logprob(rows=1 << 22, vocab=524288, stride=524288, type=FP32) == -2
     for t in (0.0, -1.0, float("nan"), float("inf"), 1e-39, 1e39):
         assert logprob(temp=t) == -4
     assert logprob(logits=None) == -1 and logprob(logits=ODD) == -3 and logprob(logits=P(0x10002), type=FP32) == -3
@@ -99,6 +99,7 @@ def test_int8_refusals():
     def prod(a=A, sa=A, b=A, sb=A, bias=None, m=4, n=5, k=100, out=A, type=BF16, os=5, ws=A, wsb=1 << 24):
         return lib.flashopt_int8_matmul(a, sa, b, sb, bias, m, n, k, out, type, os, ws, wsb, None)
     assert prod(m=0) == 0 and prod(n=0) == 0 and prod(m=-1) == -2 and prod(k=0) == -2 and prod(k=131073) == -2
+    assert prod(m=1 << 24, n=1 << 24, os=1 << 24) == -2
     assert prod(os=4) == -2 and prod(type=3) == -4 and prod(n=(1 << 24) + 1, os=1 << 25) == -2
     assert prod(a=None) == -1 and prod(sa=None) == -1 and prod(b=None) == -1 and prod(sb=None) == -1
     assert prod(out=None) == -1 and prod(a=P(0x10008)) == -3 and prod(b=P(0x10004)) == -3
