@@ -52,8 +52,7 @@ struct RowScale {
 // the largest of a block's patterns; red: one word per wave
 template <int kWaves>
 __device__ __forceinline__ uint32_t block_max(uint32_t top, uint32_t* red) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+    top = wave_max_u32(top);
     if (kWaves == 1) return top;
     if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave] = top;
     __syncthreads();
@@ -622,8 +621,7 @@ __global__ __launch_bounds__(kSkinnyWaves * kWave) void few_kernel(
 #pragma unroll
         for (int e = 0; e < E; ++e) top = max(top, as_u32(Elem<kType>::get(v, e)) & 0x7FFFFFFFu);
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+    top = wave_max_u32(top);
     if (lane == 0) red[wave] = top;
     __syncthreads();
     for (int q = 0; q < each; ++q) top = max(top, red[row * each + q]);

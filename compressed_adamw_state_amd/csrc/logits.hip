@@ -159,8 +159,7 @@ __device__ __noinline__ void search_top(const Segment<kType>& seg, uint32_t need
         const uint64_t trial = bound | (uint64_t(1) << bit);
         uint32_t n = 0;
         each([&](uint64_t x) { n += x >= trial ? 1u : 0u; });
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) n += __shfl_xor((int)n, o);
+        n = wave_reduce(n, 0u, [](uint32_t a, uint32_t b) { return a + b; });
         if (lane == 0) sh.count[turn][wave] = n;
         __syncthreads();
         uint32_t all = 0;
@@ -619,74 +618,60 @@ __global__ __launch_bounds__(kBlock) void prob_kernel(RowsIn<kType> in, ProbOut 
     }
 }
 
-// The rows of several segments joined, one block a row.  The segments' lists
-// are candidates of the row's: their entries with the value's upper 16 bits
-// at or above the top-th largest of those, ranked against each other; if too
-// many are equal there, the lists are walked from their heads instead.
-constexpr int kJoinEntries = kMaxSegments * FLASHOPT_TOP_MAX / kBlock;       // per thread
-
+// The rows of several segments joined, one block of one wave a row.  Of the
+// segments' lists, best first, the entries at or above a bound are ranked against
+// each other: with r = ceil(top / nseg), the ceil(top / r)-th largest of the
+// lists' r-th entries has that many times r entries at or above it.  If they are
+// too many (equal ones), the lists are walked from their heads instead.
 template <int kType>
-__global__ __launch_bounds__(kBlock) void prob_join_kernel(RowsIn<kType> in, ProbOut out, int top,
-                                                           const Part* part,
-                                                           const uint64_t* lists) {
-    __shared__ uint32_t count[2][kWavesPerBlock];
-    __shared__ uint64_t found[kBlock];
-    __shared__ uint32_t nfound;
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+__global__ __launch_bounds__(kWave) void prob_join_kernel(RowsIn<kType> in, ProbOut out, int top,
+                                                          const Part* part,
+                                                          const uint64_t* lists) {
+    constexpr int kMost = 256;
+    __shared__ uint64_t found[kMost];
+    const int lane = threadIdx.x;
     const int64_t row = blockIdx.x;
     const int total = in.nseg * top;
     const uint64_t* list = lists + row * total;
-    uint64_t e[kJoinEntries];
-    if (top > 0)
-#pragma unroll
-        for (int i = 0; i < kJoinEntries; ++i) {
-            const int at = i * kBlock + threadIdx.x;
-            e[i] = at < total ? list[at] : 0;
-        }
+    const int r = top > 0 ? (top + in.nseg - 1) / in.nseg : 1;
+    // 0 past a segment's entries: such lists do not count
+    const uint64_t mine = top > 0 && lane < in.nseg ? list[lane * top + r - 1] : 0;
+    const Given t = given_token<kType>(in.logits + row * in.stride, in.vocab, row, out.targets);
     const ProbStats st = prob_stats(join_parts(part + row * in.nseg, in.nseg, in.c));
-    if (threadIdx.x == 0) {
-        nfound = 0;
-        const typename Elem<kType>::T* x = in.logits + row * in.stride;
-        write_prob(row, in.c, st, given_token<kType>(x, in.vocab, row, out.targets), out);
-    }
+    if (lane == 0) write_prob(row, in.c, st, t, out);
     if (top == 0) return;
+    const uint32_t want = (uint32_t)((top + r - 1) / r), key = (uint32_t)(mine >> 48);
     uint32_t bound = 0;
+#pragma unroll
     for (int bit = 15; bit >= 0; --bit) {
         const uint32_t trial = bound | (1u << bit);
-        uint32_t n = 0;
-#pragma unroll
-        for (int i = 0; i < kJoinEntries; ++i)
-            if (i * kBlock < total) n += __popcll(__ballot((uint32_t)(e[i] >> 48) >= trial));
-        if (lane == 0) count[bit & 1][wave] = n;
-        __syncthreads();
-        n = 0;
-#pragma unroll
-        for (int w = 0; w < kWavesPerBlock; ++w) n += count[bit & 1][w];
-        if (n >= (uint32_t)top) bound = trial;
+        if ((uint32_t)__popcll(__ballot(key >= trial)) >= want) bound = trial;
     }
-#pragma unroll
-    for (int i = 0; i < kJoinEntries; ++i)
-        if (i * kBlock < total && e[i] != 0 && (uint32_t)(e[i] >> 48) >= bound) {
-            const uint32_t at = atomicAdd(&nfound, 1u);
-            if (at < (uint32_t)kBlock) found[at] = e[i];
-        }
+    uint32_t n = 0;
+    for (int at = 0; at < total; at += kWave) {
+        const uint64_t e = at + lane < total ? list[at + lane] : 0;
+        const bool is = e != 0 && (uint32_t)(e >> 48) >= bound;
+        const uint64_t who = __ballot(is);
+        const uint32_t k = n + __popcll(who & ((uint64_t(1) << lane) - 1));
+        if (is && k < (uint32_t)kMost) found[k] = e;
+        n += __popcll(who);
+    }
     __syncthreads();
-    const uint32_t n = nfound;
-    if (n <= (uint32_t)kBlock) {
-        if (threadIdx.x < n) {
-            const uint64_t x = found[threadIdx.x];
+    if (n <= (uint32_t)kMost) {
+        for (uint32_t q = lane; q < n; q += kWave) {
+            const uint64_t x = found[q];
             uint32_t rank = 0;
+#pragma unroll 4
             for (uint32_t j = 0; j < n; ++j) rank += found[j] > x ? 1u : 0u;
             if (rank < (uint32_t)top) write_top(out, row, top, (int)rank, x, in.c, st);
         }
-    } else if (wave == 0) {
-        // lane b walks the list of segment b, best first (a row has at most 64)
-        const uint64_t* mine = list + (int64_t)lane * top;
+    } else {
+        // lane b walks the list of segment b (a row has at most 64)
         int at = 0;
-        uint64_t head = lane < in.nseg ? mine[0] : 0;
+        uint64_t head = lane < in.nseg ? list[lane * top] : 0;
         for (int k = 0; k < top; ++k) {
             const uint64_t best = wave_max_u64(head);
-            if (head == best && lane < in.nseg) head = ++at < top ? mine[at] : 0;
+            if (head == best && lane < in.nseg) head = ++at < top ? list[lane * top + at] : 0;
             if (lane == 0) write_top(out, row, top, k, best, in.c, st);
         }
     }
@@ -944,8 +929,8 @@ static int launch_prob(const Rows& a, const ProbOut& out, int32_t top, void* wor
             hipLaunchKernelGGL((prob_kernel<kType, kVecs, false, 0>), grid, dim3(kBlock), 0, st, in,
                                out, 0, part, lists, none);
         if (k.nseg > 1)
-            hipLaunchKernelGGL((prob_join_kernel<kType>), dim3((unsigned)a.rows), dim3(kBlock), 0,
-                               st, in, out, top, part, lists);
+            hipLaunchKernelGGL((prob_join_kernel<kType>), dim3((unsigned)a.rows), dim3(kWave), 0, st,
+                               in, out, top, part, lists);
     });
 }
 
@@ -978,7 +963,7 @@ static int launch_prob_both(const Rows& a, const ProbOut& out, void* workspace, 
     first.stats = (ProbStats*)((char*)workspace + parts_bytes(k, a.rows));
     by_type(a.type, k.vecs, [&](auto t, auto) {
         constexpr int kType = decltype(t)::value;
-        hipLaunchKernelGGL((prob_join_kernel<kType>), dim3((unsigned)a.rows), dim3(kBlock), 0, st,
+        hipLaunchKernelGGL((prob_join_kernel<kType>), dim3((unsigned)a.rows), dim3(kWave), 0, st,
                            rows_in<kType>(a, k), first, 0, part, nullptr);
     });
     return launch_prob_grad(a, k, none, nullptr, (const float*)first.stats, g, st);

@@ -108,15 +108,36 @@ __device__ __forceinline__ void store_vec(typename Elem<kType>::T* row, int64_t 
     }
 }
 
+// Reductions over a wave by data-parallel moves: within rows of 16 lanes (shift
+// right by 1, 2, 4, 8), then each odd row takes its lower neighbour's last lane and
+// the upper half lane 31's, so that lane 63 has all.  About 8 cycles a move,
+// where a shuffle through LDS takes about 100.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ uint32_t lane_move(uint32_t none, uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)x, kCtrl, kRows, 0xF, false);
+}
+template <typename F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t x, uint32_t none, F f) {
+    x = f(x, lane_move<0x111, 0xF>(none, x));
+    x = f(x, lane_move<0x112, 0xF>(none, x));
+    x = f(x, lane_move<0x114, 0xF>(none, x));
+    x = f(x, lane_move<0x118, 0xF>(none, x));
+    x = f(x, lane_move<0x142, 0xA>(none, x));
+    x = f(x, lane_move<0x143, 0xC>(none, x));
+    return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
 __device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
-    return x;
+    return as_f32(wave_reduce(as_u32(x), 0xFF800000u, [](uint32_t a, uint32_t b) {
+        return as_u32(fmaxf(as_f32(a), as_f32(b)));
+    }));
 }
 __device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
-    return x;
+    return as_f32(wave_reduce(as_u32(x), 0u, [](uint32_t a, uint32_t b) {
+        return as_u32(as_f32(a) + as_f32(b));
+    }));
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
+    return wave_reduce(x, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
 __device__ __forceinline__ uint64_t wave_max_u64(uint64_t x) {
 #pragma unroll
