@@ -414,6 +414,7 @@ struct ProbCoef {
     float A, B, gl, low;
     __device__ __forceinline__ ProbCoef(const ProbStats& st, float c, float gl_, float gh)
         : h(st.m, c, st.l2s), gl(gl_) {
+        if (st.on == 0.0f) gh = 0.0f;            // whatever the upstream gradient
         A = -gl - gh * st.entropy;
         B = -gh * kLn2;
         low = -200.0f;
@@ -825,10 +826,17 @@ static int check_rows(const void* logits, int32_t type, int64_t rows, int64_t vo
     return FLASHOPT_OK;
 }
 
-static int check_grad(const void* grad, int32_t type, int64_t vocab, int64_t grad_stride) {
+// The gradient takes the logits' place exactly or shares nothing with them: rows
+// are read again after others' gradients have been written.
+static int check_grad(const void* logits, int32_t type, int64_t rows, int64_t vocab,
+                      int64_t stride, const void* grad, int64_t grad_stride) {
     if (!grad) return FLASHOPT_ERR_NULL;
     if (grad_stride < vocab || grad_stride > kMaxNumel) return FLASHOPT_ERR_SIZE;
-    if (!aligned(grad, type_size(type))) return FLASHOPT_ERR_ALIGN;
+    const int64_t size = (int64_t)type_size(type);
+    if (!aligned(grad, size)) return FLASHOPT_ERR_ALIGN;
+    const bool same = grad == logits && (grad_stride == stride || rows == 1);
+    if (!same && overlap(rows, logits, stride * size, vocab * size, grad, grad_stride * size, vocab * size))
+        return FLASHOPT_ERR_ARG;
     return FLASHOPT_OK;
 }
 
@@ -1057,7 +1065,7 @@ int flashopt_logprob_backward(const void* logits, int32_t type, int64_t rows, in
     if (!aligned(stats, 16) || !aligned(targets, 8) || !aligned(grad_logprob, 4) ||
         !aligned(grad_entropy, 4))
         return FLASHOPT_ERR_ALIGN;
-    const int g = check_grad(grad, type, vocab, grad_stride);
+    const int g = check_grad(logits, type, rows, vocab, stride, grad, grad_stride);
     if (g) return g;
     return launch_prob_grad({logits, type, rows, vocab, stride, temperature},
                             cut_rows(type, rows, vocab),
@@ -1077,7 +1085,7 @@ int flashopt_logprob_grad(const void* logits, int32_t type, int64_t rows, int64_
     if (!aligned(targets, 8) || !aligned(logprob, 4) || !aligned(entropy, 4) ||
         !aligned(grad_logprob, 4) || !aligned(grad_entropy, 4))
         return FLASHOPT_ERR_ALIGN;
-    const int g = check_grad(grad, type, vocab, grad_stride);
+    const int g = check_grad(logits, type, rows, vocab, stride, grad, grad_stride);
     if (g) return g;
     const int w = check_workspace(workspace, workspace_bytes,
                                   flashopt_logprob_workspace_bytes(type, rows, vocab, 0));
@@ -1125,7 +1133,7 @@ int flashopt_distill_backward(const void* logits, int32_t type, int64_t rows, in
     if (l) return l;
     if (!stats || !grad_loss) return FLASHOPT_ERR_NULL;
     if (!aligned(stats, 16) || !aligned(grad_loss, 4)) return FLASHOPT_ERR_ALIGN;
-    const int g = check_grad(grad, type, vocab, grad_stride);
+    const int g = check_grad(logits, type, rows, vocab, stride, grad, grad_stride);
     if (g) return g;
     return launch_distill_grad({logits, type, rows, vocab, stride, temperature},
                                cut_rows(type, rows, vocab), {top_id, top_logprob, top, 1}, nullptr,
@@ -1148,7 +1156,7 @@ int flashopt_distill_grad(const void* logits, int32_t type, int64_t rows, int64_
     if (l) return l;
     if (!grad_loss) return FLASHOPT_ERR_NULL;
     if (!aligned(loss, 4) || !aligned(grad_loss, 4)) return FLASHOPT_ERR_ALIGN;
-    const int g = check_grad(grad, type, vocab, grad_stride);
+    const int g = check_grad(logits, type, rows, vocab, stride, grad, grad_stride);
     if (g) return g;
     const int w = check_workspace(workspace, workspace_bytes,
                                   flashopt_distill_workspace_bytes(type, rows, vocab));

@@ -142,7 +142,7 @@ __global__ __launch_bounds__(kWaves * kWave, 4) void row_kernel(RowArgs<kType> a
         const ProbStats st = prob_stats(all);
         if (tid == 0) write_prob(row, c, st, t, a.out);
         const float gl = t.id >= 0 && st.on != 0.0f && a.up ? a.up[row] * a.inv_t : 0.0f;
-        const float gh = kEntropy ? a.up_entropy[row] * a.inv_t : 0.0f;
+        const float gh = kEntropy && st.on != 0.0f ? a.up_entropy[row] * a.inv_t : 0.0f;
         const float A = -gl - gh * st.entropy, B = -gh * kLn2, base = st.m, l2 = st.l2s;
         auto value = [&](float v) {
             const float d = __builtin_fmaf(v - base, c, -l2), p = exp2_hw(d);

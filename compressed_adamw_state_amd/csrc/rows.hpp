@@ -160,4 +160,18 @@ static inline bool valid_type(int32_t type) {
 }
 static inline size_t type_size(int32_t type) { return type == FLASHOPT_FP32 ? 4 : 2; }
 
+// Whether two matrices of `rows` rows (strides and row lengths in bytes) have a
+// byte in common.  Rows that lie between each other's are told apart where the
+// strides are equal; overlapping spans of other strides count as shared.
+static inline bool overlap(int64_t rows, const void* a, int64_t a_stride, int64_t a_bytes,
+                           const void* b, int64_t b_stride, int64_t b_bytes) {
+    typedef __int128 Wide;                       // rows * stride may pass 64 bits
+    const Wide p = (uintptr_t)a, q = (uintptr_t)b;
+    if (p + (Wide)(rows - 1) * a_stride + a_bytes <= q || q + (Wide)(rows - 1) * b_stride + b_bytes <= p)
+        return false;
+    if (a_stride != b_stride || rows == 1) return true;
+    const Wide d = ((q - p) % a_stride + a_stride) % a_stride;
+    return d < a_bytes || a_stride - d < b_bytes;
+}
+
 }  // namespace flashopt

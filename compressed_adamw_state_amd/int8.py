@@ -82,7 +82,7 @@ def int8_linear(x: torch.Tensor, weight: Int8Weight, bias: Optional[torch.Tensor
     k, n, dev = weight.k, weight.n, weight.codes.device
     if x.shape[-1] != k:
         raise ValueError(f"x has {x.shape[-1]} features, the weight {k}")
-    if x.requires_grad and torch.is_grad_enabled():
+    if (x.requires_grad or (bias is not None and bias.requires_grad)) and torch.is_grad_enabled():
         raise ValueError("int8_linear has no gradient: call it under torch.no_grad()")
     if x.device != dev or not x.is_cuda:
         raise ValueError("x and the weight must be on one GPU")
@@ -128,6 +128,15 @@ class Int8Linear(torch.nn.Module):
     @classmethod
     def from_linear(cls, linear: torch.nn.Linear) -> "Int8Linear":
         return cls(Int8Weight.from_weight(linear.weight), linear.bias)
+
+    def _apply(self, fn, recurse: bool = True):
+        # a model's .to(dtype), .half() and .bfloat16() change the bias alone:
+        # the scales stay the FP32 numbers they are
+        scale = self.scale
+        super()._apply(fn, recurse)
+        if self.scale.dtype != torch.float32:
+            self.scale = scale.to(self.scale.device)
+        return self
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         return int8_linear(x, Int8Weight(self.codes, self.scale, self.in_features), self.bias)

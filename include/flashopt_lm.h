@@ -10,7 +10,10 @@
  * launch (a failed call launches nothing), no synchronisation, no C++
  * exception.  Every call may be captured into a HIP graph.  A workspace is
  * written and read by its call only: calls that may overlap (other streams,
- * graphs replayed at the same time) need workspaces of their own.
+ * graphs replayed at the same time) need workspaces of their own.  No output
+ * may share memory with an input, except a gradient that takes its logits'
+ * place; a gradient or layer output that overlaps its logits or input
+ * otherwise is refused (FLASHOPT_ERR_ARG).
  */
 #ifndef FLASHOPT_LM_H
 #define FLASHOPT_LM_H
@@ -127,7 +130,7 @@ int flashopt_distill_grad(const void* logits, int32_t type, int64_t rows, int64_
  * row holding an infinity or NaN has codes 0 and scale NaN, so that all that
  * is computed from it is NaN.  Codes are 16-byte aligned, scales 4.
  * Limits: rows <= 2^24, cols <= FLASHOPT_INT8_COLS_MAX (so that a sum of products
- * fits a 32-bit integer); a product m n <= 2^44. */
+ * fits a 32-bit integer); a product (m/128 + 1)(n/128 + 1) <= 2^30. */
 #define FLASHOPT_INT8_COLS_MAX 131072
 int64_t flashopt_int8_ld(int64_t cols);
 /* From rows x cols values of `type`, row stride `stride` elements. */
@@ -141,7 +144,8 @@ int flashopt_tensor_quantize_rows(const flashopt_tensor* t, int32_t kind, int64_
 /* out[i][j] = RN_type(a_scale[i] * b_scale[j] * sum_c a[i][c] b[j][c] + bias[j]):
  * a is m x k (tokens), b n x k (output channels), both as above; bias (of
  * out_type) may be NULL; out row i at element i * out_stride, out_stride >= n.
- * The sum is an exact 32-bit integer. */
+ * The sum is an exact 32-bit integer; the scales' product is formed first, in
+ * binary32. */
 size_t flashopt_int8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
 int flashopt_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b,
                          const float* b_scale, const void* bias, int64_t m, int64_t n, int64_t k,

@@ -394,6 +394,39 @@ def test_gradient_in_the_logits_place_of_cut_rows():
             assert torch.equal(r.grad, b)
 
 
+def test_gradient_beside_the_logits():
+    """Rows of logits and of their gradient by turns in one buffer: no row touches another's."""
+    for rows, vocab in ((3, 50257), (300, 9000)):
+        x, t, g = draw(rows, vocab, torch.bfloat16, vocab)
+        both = torch.zeros(rows, 2, vocab, dtype=torch.bfloat16, device="cuda")
+        both[:, 0] = x.cuda()
+        up = torch.randn(rows, generator=g).cuda()
+        want = L.token_logprobs_grad(x.cuda(), t.cuda(), up, up).grad
+        F.flashopt_logprob_grad(both[:, 0], t.cuda(), up, up, both[:, 1])
+        assert torch.equal(both[:, 1], want) and torch.equal(both[:, 0].cpu(), x)
+        with pytest.raises(F.FlashoptError):
+            F.flashopt_logprob_grad(both[:, 0], t.cuda(), up, up, both.view(rows, -1)[:, 1:vocab + 1])
+
+
+@pytest.mark.parametrize("rows,vocab", [(3, 90001), (3, 1000), (300, 9000)])
+def test_rows_without_a_distribution_ignore_their_upstream(rows, vocab):
+    """Cut rows, whole rows, rows in registers: nothing but -inf gives a gradient of 0, whatever
+    the upstream gradients."""
+    x = torch.randn(rows, vocab, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    x[1] = -math.inf
+    t = torch.full((rows,), 5, device="cuda")
+    up = torch.ones(rows, device="cuda")
+    up[1] = math.nan
+    xg = x.clone().requires_grad_()
+    r = L.token_logprobs(xg, t)
+    grads = [L.token_logprobs_grad(x, t, up, up).grad, L.token_logprobs_grad(x, t, up).grad,
+             torch.autograd.grad((r.logprob, r.entropy), xg, (up, up))[0]]
+    for tail in (False, True):
+        grads.append(L.distill_grad(x, t.view(rows, 1), -up.view(rows, 1).nan_to_num(0.5), up, tail=tail)[1])
+    for gr in grads:
+        assert bool((gr[1] == 0).all()) and bool(torch.isfinite(gr).all())
+
+
 def test_in_place_refuses_a_stale_backward():
     """torch's graph sees that the logits' values are gone."""
     x = torch.randn(4, 100, device="cuda", requires_grad=True)

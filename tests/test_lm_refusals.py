@@ -120,6 +120,41 @@ def test_int8_refusals():
     assert lib.flashopt_int8_workspace_bytes(4, 5, 0) == 0 and lib.flashopt_int8_workspace_bytes(9, 5, 100) > 0
 
 
+def test_overlapping_outputs_are_refused():
+    """A gradient that overlaps its logits other than in their place, a layer's output that
+    overlaps its input; rows that lie between each other's are no overlap (they then fail later
+    validation here: nothing is launched)."""
+    lib = F.lib()
+
+    def grads(grad, gs, stride=300, rows=4, up=A):
+        yield lib.flashopt_logprob_backward(A, BF16, rows, 100, stride, 1.0, A, A, up, None, grad, gs, None)
+        yield lib.flashopt_logprob_grad(A, BF16, rows, 100, stride, 1.0, A, up, None, A, 1 << 20, A, A, grad, gs, None)
+        yield lib.flashopt_distill_backward(A, BF16, rows, 100, stride, 1.0, A, A, 4, A, up, grad, gs, None)
+        yield lib.flashopt_distill_grad(A, BF16, rows, 100, stride, 1.0, A, A, 4, 1, up, A, 1 << 20, A, grad, gs, None)
+
+    for grad, gs in ((P(0x10000 + 198), 300), (P(0x10000 - 198), 300), (P(0x10000 + 402), 300), (A, 301), (A, 100),
+                     (P(0x10000 + 600), 300), (P(0x10000 - 600), 300), (P(0x10000 + 1200), 400)):
+        assert set(grads(grad, gs)) == {-4}
+    assert set(grads(P(0x10000 + 2), 100, rows=1)) == {-4}
+
+    def lin(out, os=500, m=9, k=100, xs=500, n=50, type=BF16):
+        return lib.flashopt_int8_linear(A, type, m, k, xs, P(0x900000), P(0x800000), None, n, out, os,
+                                        P(0xA00000), 1 << 24, None)
+    for m in (1, 9):
+        assert lin(A, m=m) == -4 and lin(P(0x10000 + 198), m=m) == -4 and lin(P(0x10000 - 98), m=m) == -4
+        assert lin(P(0x10000 + 100), os=60, m=m) == -4 and lin(P(0x10000 + 396), m=m, type=FP32) == -4
+    assert lin(P(0x10000 + 1000 - 98)) == -4
+
+
+def test_a_frozen_layer_keeps_its_scales():
+    layer = I.Int8Linear(I.Int8Weight(torch.zeros((4, 128), dtype=torch.int8), torch.full((4,), 1 / 3), 10), torch.ones(4))
+    layer = torch.nn.Sequential(layer).to(torch.bfloat16).half()[0]
+    assert torch.equal(layer.scale, torch.full((4,), 1 / 3)) and layer.bias.dtype == torch.float16
+    assert layer.codes.dtype == torch.int8 and set(layer.state_dict()) == {"codes", "scale", "bias"}
+    with pytest.raises(ValueError):                       # a bias that would want a gradient
+        I.int8_linear(torch.zeros(2, 10), I.Int8Weight(layer.codes, layer.scale, 10), torch.zeros(4, requires_grad=True))
+
+
 def test_python_refusals():
     x = torch.zeros(4, 10)
     t = torch.zeros(4, dtype=torch.int64)
