@@ -674,6 +674,15 @@ static int check_outputs(int64_t m, int64_t n) {
     return (m / 128 + 1) * (n / 128 + 1) > (int64_t(1) << 30) ? FLASHOPT_ERR_SIZE : FLASHOPT_OK;
 }
 
+// x is read after the first outputs have been written: every block of
+// few_kernel rounds it for itself
+static int check_apart(int32_t type, int64_t m, const void* x, int64_t x_stride, int64_t k,
+                       const void* out, int64_t out_stride, int64_t n) {
+    const int64_t size = (int64_t)type_size(type);
+    return overlap(m, x, x_stride * size, k * size, out, out_stride * size, n * size)
+               ? FLASHOPT_ERR_ARG : FLASHOPT_OK;
+}
+
 static int check_codes(const void* codes, const void* scale) {
     if (!codes || !scale) return FLASHOPT_ERR_NULL;
     if (!aligned(codes, 16) || !aligned(scale, 4)) return FLASHOPT_ERR_ALIGN;
@@ -739,27 +748,35 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k) {
     const int64_t stages = ld_of(k) / kStage;
     const int64_t tn = (n + SmallTile::BN - 1) / SmallTile::BN, tm = (m + SmallTile::BM - 1) / SmallTile::BM;
     const int64_t tiles = tn * tm, large = ((n + 255) / 256) * ((m + 255) / 256);
-    // Up to 16 tokens the weights' own rate decides.  Up to 64 the tokens read
-    // again for every 16 channels count, but tiles need channels to fill the
-    // GPU: 32 tokens, 14336 x 4096: 27.7 us here, 24.6 in tiles; 4096 x 14336: 26
-    // and, even split, 34.
-    // (64 tokens of 4096 x 4096: 16 us, 22 in tiles)
-    p.skinny = m <= 16 ? 1 : m <= 32 && tn < 96 ? 2 : m <= 64 && tn < 96 ? 4 : 0;
-    if (p.skinny) return p;
     // 4096 x 4096 x 4096 in large tiles: 64 us; 2048 x 4096 x 4096 in small ones 40
-    // for 47, 1024 x 5120 x 5120 40 for 63
-    if (large >= 200) {
+    // for 47, 1024 x 5120 x 5120 40 for 63.  Half of a large tile is waste up to 128
+    // rows of a side: 64 tokens, 128256 x 4096: 127 us in small ones for 144; 150: 165
+    // for 150.
+    if (large >= 200 && m > 128 && n > 128) {
         p.way = Plan::kLarge;
         return p;
     }
-    p.way = Plan::kSmall;
     // Pieces of at least 8 stages, until a block runs on each CU, if that gains:
     // a stage takes about half a microsecond of a block alone on its CU, another
     // launch 6, a piece's sums 1/32.  100 tokens, 4096 x 14336 (32 tiles): 34 us
     // for 66; 1024 x 4096 (8 tiles): 20 for 24; but 128 tokens, 14336 x 4096 (112
     // tiles): 31 for 22.
     const int64_t q = 256 / tiles < stages / 8 ? 256 / tiles : stages / 8;
-    if (q >= 2 && stages * (q - 1) * 16 > q * (192 + tiles * q)) {
+    const bool split = q >= 2 && stages * (q - 1) * 16 > q * (192 + tiles * q);
+    // Up to 16 tokens the weights' own rate decides.  Up to 64 the tokens read
+    // again for every 16 channels count, and tiles need channels to fill the GPU:
+    // each way's time in 1/256 us, fitted to 180 sizes of 17 to 64 tokens, 768 to
+    // 11264 channels and rows of 768 to 28672.  Within 18% of the better way at
+    // each (14.9 us for 12.7 at worst), 0.2% over them all; 64 tokens of 4096 x
+    // 4096: 12 us here, 18 in tiles; of 4096 x 14336: 40 and 27.
+    const int64_t here = 512 + stages * (m + 26) * (n > 4096 ? n : 4096) / 4096;
+    const int64_t in_tiles = split ? 3840 + 205 * stages / q : 1024 + 192 * stages;
+    if (m <= 16 || (m <= 64 && tn < 96 && here <= in_tiles)) {
+        p.skinny = m <= 16 ? 1 : m <= 32 ? 2 : 4;
+        return p;
+    }
+    p.way = Plan::kSmall;
+    if (split) {
         p.way = Plan::kSplit;
         p.splits = q;
         p.sums = (size_t)(tiles * q) * (SmallTile::BN * SmallTile::BM * sizeof(int));
@@ -926,6 +943,7 @@ int flashopt_int8_linear(const void* x, int32_t type, int64_t m, int64_t k, int6
     if (few_tokens(m, n, k)) {
         const int e = check_product(w, w_scale, w, w_scale, bias, out, type);
         if (e) return e;
+        if (check_apart(type, m, x, x_stride, k, out, out_stride, n)) return FLASHOPT_ERR_ARG;
         return by_type(type, [&](auto t) {
             constexpr int kType = decltype(t)::value;
             typedef typename Elem<kType>::T T;
@@ -944,6 +962,7 @@ int flashopt_int8_linear(const void* x, int32_t type, int64_t m, int64_t k, int6
     float* scale = (float*)(codes + up256((size_t)(m * ld_of(k))));
     const int e = check_product(codes, scale, w, w_scale, bias, out, type);
     if (e) return e;
+    if (check_apart(type, m, x, x_stride, k, out, out_stride, n)) return FLASHOPT_ERR_ARG;
     const int q = launch_quantize(x, type, m, k, x_stride, codes, scale, st);
     if (q) return q;
     return launch_matmul(plan, codes, scale, w, w_scale, bias, m, n, k, out, type, out_stride,

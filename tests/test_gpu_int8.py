@@ -192,3 +192,25 @@ def test_captured_and_replayed():
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(held, eager)
+
+
+def test_output_beside_the_input():
+    """Rows of input and output by turns in one buffer; an output over its input is refused."""
+    w = I.Int8Weight.from_weight(draw(96, 200, torch.bfloat16, 5).cuda())
+    for m in (2, 40):
+        x = draw(m, 200, torch.bfloat16, m).cuda()
+        both = torch.zeros(m, 296, dtype=torch.bfloat16, device="cuda")
+        both[:, :200] = x
+        I.int8_linear(both[:, :200], w, out=both[:, 200:])
+        assert torch.equal(both[:, 200:], I.int8_linear(x, w)) and torch.equal(both[:, :200], x)
+        with pytest.raises(F.FlashoptError):
+            I.int8_linear(both[:, :200], w, out=both[:, 199:295])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m,n,k", [(20, 70000, 130), (40, 300, 14336), (64, 4096, 8193), (48, 12289, 640), (70000, 20, 130),
+                                   (128, 33000, 129), (129, 25700, 130)])
+def test_linear_of_few_rows_or_channels(dtype, m, n, k):
+    """Up to 128 rows of a side in small tiles, more of them than blocks; few tokens cut along
+    the row; just past either."""
+    test_linear(dtype, m, n, k)
