@@ -515,41 +515,65 @@ __global__ __launch_bounds__(WN * WM * kWave) void join_kernel(
 constexpr int kSkinnyWaves = 8;
 
 // What a block's waves leave: their sums of 16 channels x 16 MT tokens.
-template <int MT>
+template <int MT, int kWaves>
 struct SkinnySums {
-    int v[kSkinnyWaves][MT][16][17];
+    int v[kWaves][MT][16][17];
 };
 
-template <int kType, int MT>
-__device__ __forceinline__ void skinny_out(SkinnySums<MT>& sums, const i32x4* acc, const float* scale,
-                                           const float* b_scale, const typename Elem<kType>::T* bias,
-                                           int m, int64_t n0, int64_t n,
-                                           typename Elem<kType>::T* out, int64_t out_stride) {
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+// A block's output.  A thread's entries are of channel n0 + threadIdx.x % 16, whose
+// scale and bias are loaded before the weights, as loads come back in order
+// (behind them: 14.5 us for 12.5 at 16 tokens, 50257 x 768), and so are its
+// tokens' scales, where they do not come from LDS.
+template <int kType, int MT, int kWaves>
+struct SkinnyOut {
+    static constexpr int kRows = kWaves * 4, kEach = (MT * 16 + kRows - 1) / kRows;
+    float channel, bias, token[kEach];
+    int m;
+    int64_t n0, n;
+
+    __device__ __forceinline__ SkinnyOut(const float* a_scale, const float* b_scale,
+                                         const typename Elem<kType>::T* b, int m_, int64_t n0_,
+                                         int64_t n_)
+        : m(m_), n0(n0_), n(n_) {
+        const int64_t j = min(n0 + (threadIdx.x & 15), n - 1);
+        channel = b_scale[j];
+        bias = b ? Elem<kType>::up(b[j]) : 0.0f;
+        if (a_scale)
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sums.v[wave][t][lane & 15][(lane >> 4) * 4 + r] = acc[t][r];
-    __syncthreads();
-    for (int q = threadIdx.x; q < MT * 256; q += kSkinnyWaves * kWave) {
-        const int t = q / 256, i = q % 256 / 16, j = q % 16;
-        if (t * 16 + i >= m || n0 + j >= n) continue;
-        int sum = 0;
-#pragma unroll
-        for (int v = 0; v < kSkinnyWaves; ++v) sum += sums.v[v][t][i][j];
-        float y = (float)sum * (scale[t * 16 + i] * b_scale[n0 + j]);
-        if (bias) y += Elem<kType>::up(bias[n0 + j]);
-        out[(int64_t)(t * 16 + i) * out_stride + n0 + j] = Elem<kType>::down(y);
+            for (int r = 0; r < kEach; ++r) token[r] = a_scale[min(r * kRows + (int)threadIdx.x / 16, m - 1)];
+        __builtin_amdgcn_sched_barrier(0);
     }
-}
+    __device__ __forceinline__ void write(SkinnySums<MT, kWaves>& sums, const i32x4* acc,
+                                          typename Elem<kType>::T* out, int64_t out_stride,
+                                          const float* scale = nullptr) const {
+        const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sums.v[wave][t][lane & 15][(lane >> 4) * 4 + r] = acc[t][r];
+        __syncthreads();
+        const int j = threadIdx.x & 15;
+#pragma unroll
+        for (int r = 0; r < kEach; ++r) {
+            const int i = r * kRows + threadIdx.x / 16;
+            if (i >= m || i >= MT * 16 || n0 + j >= n) continue;
+            int sum = 0;
+#pragma unroll
+            for (int v = 0; v < kWaves; ++v) sum += sums.v[v][i / 16][i % 16][j];
+            out[(int64_t)i * out_stride + n0 + j] =
+                Elem<kType>::down((float)sum * ((scale ? scale[i] : token[r]) * channel) + bias);
+        }
+    }
+};
 
 // A wave's share of a row, in lines of 128 codes.
+template <int kWaves>
 struct SkinnyShare {
     int k, end;
     __device__ __forceinline__ SkinnyShare(int32_t ld, int wave) {
         const int lines = ld / 128;
-        k = lines * wave / kSkinnyWaves * 128;
-        end = lines * (wave + 1) / kSkinnyWaves * 128;
+        k = lines * wave / kWaves * 128;
+        end = lines * (wave + 1) / kWaves * 128;
     }
 };
 constexpr int kSkinnyWords = 8;                  // of 64 codes, in flight at a time
@@ -559,9 +583,10 @@ __global__ __launch_bounds__(kSkinnyWaves * kWave) void skinny_kernel(
     const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
     const typename Elem<kType>::T* bias, int m, int64_t n, int32_t ld,
     typename Elem<kType>::T* out, int64_t out_stride) {
-    __shared__ SkinnySums<MT> sums;
+    __shared__ SkinnySums<MT, kSkinnyWaves> sums;
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const SkinnyOut<kType, MT, kSkinnyWaves> to(a_scale, b_scale, bias, m, n0, n);
     const int8_t* w = b + min(n0 + (lane & 15), n - 1) * ld + (lane >> 4) * 16;
     const int8_t* x[MT];
 #pragma unroll
@@ -569,7 +594,7 @@ __global__ __launch_bounds__(kSkinnyWaves * kWave) void skinny_kernel(
     i32x4 acc[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) acc[t] = i32x4{0, 0, 0, 0};
-    SkinnyShare s(ld, wave);
+    SkinnyShare<kSkinnyWaves> s(ld, wave);
     auto some = [&](auto count) {
         constexpr int L = decltype(count)::value;
         i32x4 wv[L];
@@ -584,52 +609,68 @@ __global__ __launch_bounds__(kSkinnyWaves * kWave) void skinny_kernel(
     };
     while (s.k + kSkinnyWords * 64 <= s.end) some(std::integral_constant<int, kSkinnyWords>());
     while (s.k < s.end) some(std::integral_constant<int, 2>());
-    skinny_out<kType, MT>(sums, acc, a_scale, b_scale, bias, m, n0, n, out, out_stride);
+    to.write(sums, acc, out, out_stride);
 }
 
 // The same for up to kFewTokens tokens in their own type, which each block
 // rounds for itself into LDS while its first weights are on their way: one
 // launch, no workspace.
-constexpr int kFewTokens = 4, kFewBytes = 32768;
+constexpr int kFewTokens = 4, kFewEntries = 16;  // entries of a token that a thread holds
 
-template <int kType>
-__global__ __launch_bounds__(kSkinnyWaves * kWave) void few_kernel(
+template <int kType, int kWaves>
+__global__ __launch_bounds__(kWaves * kWave) void few_kernel(
     const typename Elem<kType>::T* x, int m, int32_t cols, int64_t x_stride, const int8_t* b,
     const float* b_scale, const typename Elem<kType>::T* bias, int64_t n, int32_t ld,
     typename Elem<kType>::T* out, int64_t out_stride) {
     constexpr int E = Elem<kType>::kE;
     extern __shared__ __attribute__((aligned(16))) int8_t codes[];       // m rows of ld + 16
-    __shared__ SkinnySums<1> sums;
-    __shared__ uint32_t red[kSkinnyWaves];
+    __shared__ SkinnySums<1, kWaves> sums;
+    __shared__ uint32_t red[kWaves];
     __shared__ float scale[kFewTokens];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
+    // the waves of a row; its words and the entries behind them
+    const int each = kWaves / (m <= 1 ? 1 : m <= 2 ? 2 : 4), row = wave / each, at = wave % each * kWave + lane;
+    const int step = each * kWave, words = cols / E, left = cols % E;
+    const typename Elem<kType>::T* p = x + (int64_t)min(row, m - 1) * x_stride;
+    // The tokens' loads go first and without a branch: loads come back in order, so
+    // that their largest entry is found while the weights are still on their way.
+    // Words past the row's end read its last word again.
+    constexpr int kHeld = kFewEntries / E;
+    u32x4 xv[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        xv[i] = *reinterpret_cast<const u32x4_any*>(p + min(i * step + at, words - 1) * E);
+    const float rest = Elem<kType>::up(p[at < left ? words * E + at : 0]);
+    const SkinnyOut<kType, 1, kWaves> to(nullptr, b_scale, bias, m, n0, n);
+
     const int8_t* w = b + min(n0 + (lane & 15), n - 1) * ld + (lane >> 4) * 16;
-    SkinnyShare s(ld, wave);
+    SkinnyShare<kWaves> s(ld, wave);
     i32x4 wv[kSkinnyWords];
     const int first = s.end - s.k < kSkinnyWords * 64 ? s.end - s.k : kSkinnyWords * 64;
     // words past the share are read from its row and not used (ld is at least 128)
 #pragma unroll
     for (int i = 0; i < kSkinnyWords; ++i) wv[i] = *(const i32x4*)(w + (i * 64 < first ? s.k + i * 64 : 0));
+    __builtin_amdgcn_sched_barrier(0);
 
-    // 2, 4 or 8 waves a row
-    const int each = m <= 1 ? 8 : m <= 2 ? 4 : 2, row = wave / each, part = wave % each;
-    const typename Elem<kType>::T* p = x + (int64_t)min(row, m - 1) * x_stride;
-    uint32_t top = 0;
-    for (int j = part * kWave + lane; j * E < cols; j += each * kWave) {
-        const u32x4 v = load_vec<kType>(p, j, cols, 0);
+    uint32_t top = as_u32(rest) & 0x7FFFFFFFu;   // (or of the row's first entry)
 #pragma unroll
-        for (int e = 0; e < E; ++e) top = max(top, as_u32(Elem<kType>::get(v, e)) & 0x7FFFFFFFu);
-    }
+    for (int i = 0; i < kHeld; ++i)
+#pragma unroll
+        for (int e = 0; e < E; ++e) top = max(top, as_u32(Elem<kType>::get(xv[i], e)) & 0x7FFFFFFFu);
     top = wave_max_u32(top);
     if (lane == 0) red[wave] = top;
     __syncthreads();
     for (int q = 0; q < each; ++q) top = max(top, red[row * each + q]);
     const RowScale S(top);
     if (row < m) {
-        for (int j = part * kWave + lane; j * E < ld; j += each * kWave)
-            word_codes<kType>(load_vec<kType>(p, j, cols, 0), (int64_t)j * E, cols, S, codes + row * (ld + 16));
-        if (part == 0 && lane == 0) scale[row] = S.scale();
+        int8_t* q = codes + row * (ld + 16);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (i * step + at < words) word_codes<kType>(xv[i], (i * step + at) * E, cols, S, q);
+        if (at < left) q[words * E + at] = (int8_t)S.code(rest);
+        for (int j = cols + at; j < ld; j += step) q[j] = 0;
+        if (at == 0) scale[row] = S.scale();
     }
     __syncthreads();
     const int8_t* xl = codes + min(lane & 15, m - 1) * (ld + 16) + (lane >> 4) * 16;
@@ -650,7 +691,7 @@ __global__ __launch_bounds__(kSkinnyWaves * kWave) void few_kernel(
     };
     while (s.k + kSkinnyWords * 64 <= s.end) some(std::integral_constant<int, kSkinnyWords>());
     while (s.k < s.end) some(std::integral_constant<int, 2>());
-    skinny_out<kType, 1>(sums, &acc, scale, b_scale, bias, m, n0, n, out, out_stride);
+    to.write(sums, &acc, out, out_stride, scale);
 }
 
 template <typename F>
@@ -823,13 +864,20 @@ static int launch_matmul(const Plan& plan, const int8_t* a, const float* a_scale
     });
 }
 
-// Rounding the tokens in every block: worth a launch while the blocks run at
-// once and round little.  Measured: 1 token, 14336 x 4096 (896 blocks): 16.4 us,
-// 18.4 in two launches, 2 tokens 20.0 and 18.4; 4 tokens, 4096 x 4096: 10.4 and
-// 14.4, 8 tokens 15.2 and 14.4; 1 token, 50257 x 768 (3142 blocks): 33.6 and 15.
-static bool few_tokens(int64_t m, int64_t n, int64_t k) {
-    const int64_t blocks = (n + 15) / 16, codes = m * ld_of(k);
-    return m <= kFewTokens && codes <= kFewBytes && blocks <= 1024 && blocks * codes <= 4500000;
+// Rounding the tokens in every block saves a launch and pays while the threads
+// hold the tokens and either the blocks all run at once or the rows are long:
+// the waves of a block, 0 for two launches.  Measured, here and in two launches:
+// 1 token: 4096 x 4096 7.5 and 8.7 us, 128256 x 4096 87 and 96, 28672 x 8192 43.5
+// and 42.6, but 50257 x 768 (3142 blocks) 16.9 and 13.0; 2 tokens, 4096 x 4096: 8.2
+// and 8.6; 4 tokens, 4096 x 4096 (read twice): 10.4 and 8.9, 2304 x 768: 8.1 and 11.9.
+// Blocks of 4 waves leave room for more of them: 1 token, 14336 x 4096: 14.5 us,
+// 15.7 with 8 waves; up to one block a CU 8 waves read faster.
+static int few_waves(int64_t m, int64_t n, int64_t k) {
+    const int64_t blocks = (n + 15) / 16, rows = m <= 1 ? 1 : m <= 2 ? 2 : 4;
+    if (m > kFewTokens || k < 8 || (blocks > 1024 && k < 4096)) return 0;
+    const int64_t held = kFewEntries * kWave / rows;             // of a token, by each wave
+    if (blocks > 256 && k <= 4 * held) return 4;
+    return k <= 8 * held ? 8 : 0;
 }
 
 static size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
@@ -888,7 +936,7 @@ int flashopt_tensor_quantize_rows(const flashopt_tensor* t, int32_t kind, int64_
 }
 
 size_t flashopt_int8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-    if (check_matrix(m, k) || check_matrix(n, k) || check_outputs(m, n) || m == 0 || n == 0 || few_tokens(m, n, k)) return 0;
+    if (check_matrix(m, k) || check_matrix(n, k) || check_outputs(m, n) || m == 0 || n == 0 || few_waves(m, n, k)) return 0;
     return up256(plan_of(m, n, k).sums) + up256((size_t)(m * ld_of(k))) +
            up256((size_t)m * sizeof(float));
 }
@@ -940,7 +988,8 @@ int flashopt_int8_linear(const void* x, int32_t type, int64_t m, int64_t k, int6
     if (!x) return FLASHOPT_ERR_NULL;
     if (!aligned(x, type_size(type))) return FLASHOPT_ERR_ALIGN;
     hipStream_t st = (hipStream_t)stream;
-    if (few_tokens(m, n, k)) {
+    const int few = few_waves(m, n, k);
+    if (few) {
         const int e = check_product(w, w_scale, w, w_scale, bias, out, type);
         if (e) return e;
         if (check_apart(type, m, x, x_stride, k, out, out_stride, n)) return FLASHOPT_ERR_ARG;
@@ -948,10 +997,15 @@ int flashopt_int8_linear(const void* x, int32_t type, int64_t m, int64_t k, int6
             constexpr int kType = decltype(t)::value;
             typedef typename Elem<kType>::T T;
             const int64_t ld = ld_of(k);
-            hipLaunchKernelGGL((few_kernel<kType>), dim3((unsigned)((n + 15) / 16)),
-                               dim3(kSkinnyWaves * kWave), (size_t)(m * (ld + 16)), st, (const T*)x,
-                               (int)m, (int32_t)k, x_stride, w, w_scale, (const T*)bias, n,
-                               (int32_t)ld, (T*)out, out_stride);
+            auto launch = [&](auto waves) {
+                constexpr int kWaves = decltype(waves)::value;
+                hipLaunchKernelGGL((few_kernel<kType, kWaves>), dim3((unsigned)((n + 15) / 16)),
+                                   dim3(kWaves * kWave), (size_t)(m * (ld + 16)), st, (const T*)x,
+                                   (int)m, (int32_t)k, x_stride, w, w_scale, (const T*)bias, n,
+                                   (int32_t)ld, (T*)out, out_stride);
+            };
+            if (few == 4) launch(std::integral_constant<int, 4>());
+            else launch(std::integral_constant<int, 8>());
         });
     }
     if (!workspace) return FLASHOPT_ERR_NULL;

@@ -214,3 +214,12 @@ def test_linear_of_few_rows_or_channels(dtype, m, n, k):
     """Up to 128 rows of a side in small tiles, more of them than blocks; few tokens cut along
     the row; just past either."""
     test_linear(dtype, m, n, k)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m,n,k", [(1, 30, 7), (1, 30, 8), (1, 100, 8191), (1, 4200, 4095), (1, 17000, 4097), (1, 40, 8193),
+                                   (2, 4200, 2047), (2, 4200, 2049), (2, 33, 4096), (3, 40, 2048), (3, 5000, 1000),
+                                   (4, 4200, 1023), (4, 4200, 1025), (4, 20000, 513), (4, 31, 2049)])
+def test_linear_of_few_tokens(dtype, m, n, k):
+    """Tokens rounded by the product's own blocks of 4 or 8 waves, and just past what those hold."""
+    test_linear(dtype, m, n, k)
