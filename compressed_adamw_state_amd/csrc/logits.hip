@@ -776,15 +776,24 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(RowsIn<kType> in, 
 
 // ---- host ---------------------------------------------------------------------
 
-// How a call cuts its rows.  A block streams a segment of a row.  From
-// kBlocksWanted rows on (a block for each CU) a segment is the whole row: no
-// join, one launch.  With fewer the rows are cut until that many blocks run (at
-// most kMaxSegments a row, which one wave joins), and with very few the chunks
-// are the short ones.  Measured, 501 rows of 50257 in BF16 with the top 20: 33 us
-// whole, 38 us in two or three segments; 700 rows of 32000 in FP32: 31 and 42;
-// 128 rows of 50257: 26 us in two segments, 23 in eight.  A segment is at most
-// kMaxChunks chunks, whose maxima or marks lie in LDS.
-constexpr int64_t kBlocksWanted = 256;
+// How a call cuts its rows.  A block streams a segment of a row.  A segment is the
+// whole row (no join, one launch) from kBlocksWanted rows on, a block for each CU,
+// and for rows of up to kWholeWords words: a launch takes 4 us of host time and the
+// join 3 us of the GPU's.  Measured, the GPU's time of a graph's call, cut and
+// whole, and a call's from the host: 32 rows of 16000 in BF16: 5.7 and 4.9 us, 16.4
+// and 12.5; of 32000: 5.8 and 6.7, 16.4 and 12.5, with the gradient 6.9 and 10.5, 19.3
+// and 15.3; of 65536: 6.1 and 7.6, with the gradient 7.9 and 13.2.  Top entries cost a
+// cut row more: 32 rows of 50257, top 20: 16.3 and 14.4, 21.6 and 17.4; of 128256: 13.0
+// and 17.6.  Longer rows, if few, are cut until kBlocksWanted blocks run (at most
+// kMaxSegments a row, which one wave joins): 501 rows of 50257 in BF16 with the top
+// 20: 33 us whole, 38 us in two or three segments; 128 rows: 26 us in two
+// segments, 23 in eight.  A segment is at most kMaxChunks chunks, whose maxima or
+// marks lie in LDS.
+//
+// Chunks are the short ones where there are few of them, or where the last long
+// one of a row that is one or two would be less than 3/4 full: 32 rows of 8000 in
+// BF16: 4.2 us for 4.9, of 24000: 6.0 for 6.8, but of 32000: 6.9 for 6.7.
+constexpr int64_t kBlocksWanted = 256, kWholeWords = 4096, kWholeWordsTop = 8192;
 constexpr int kMaxChunks = 16;
 struct Cut {
     int vecs;
@@ -792,13 +801,15 @@ struct Cut {
     int32_t nseg;
     int chunks;                                  // of a segment
 };
-static Cut cut_rows(int32_t type, int64_t rows, int64_t vocab) {
+static Cut cut_rows(int32_t type, int64_t rows, int64_t vocab, int32_t top) {
     const int64_t e = type == FLASHOPT_FP32 ? 4 : 8, words = (vocab + e - 1) / e;
+    const int64_t step_long = kLong * kBlock, lng = (words + step_long - 1) / step_long;
+    const bool whole = words <= (top > 0 ? kWholeWordsTop : kWholeWords);
     Cut k;
-    const int64_t lng = (words + kLong * kBlock - 1) / (kLong * kBlock);
-    k.vecs = rows * lng < 256 ? kShort : kLong;
+    k.vecs = kLong;
+    if (whole ? lng <= 2 && (words - 1) % step_long < step_long * 3 / 4 : rows * lng < 256) k.vecs = kShort;
     const int64_t step = (int64_t)k.vecs * kBlock, chunks = (words + step - 1) / step;
-    int64_t want = (kBlocksWanted + rows - 1) / (rows < 1 ? 1 : rows);
+    int64_t want = whole ? 1 : (kBlocksWanted + rows - 1) / (rows < 1 ? 1 : rows);
     want = want < 1 ? 1 : want > kMaxSegments ? kMaxSegments : want;
     k.chunks = (int)((chunks + want - 1) / want);
     if (k.chunks > kMaxChunks) k.chunks = kMaxChunks;
@@ -809,7 +820,7 @@ static Cut cut_rows(int32_t type, int64_t rows, int64_t vocab) {
 
 // a launch has less than 2^32 threads
 static bool rows_fit(int32_t type, int64_t rows, int64_t vocab) {
-    return rows <= FLASHOPT_ROWS_MAX && rows * cut_rows(type, rows, vocab).nseg <= FLASHOPT_ROWS_MAX;
+    return rows <= FLASHOPT_ROWS_MAX && rows * cut_rows(type, rows, vocab, 0).nseg <= FLASHOPT_ROWS_MAX;
 }
 
 static int check_rows(const void* logits, int32_t type, int64_t rows, int64_t vocab, int64_t stride,
@@ -921,7 +932,7 @@ static int launch_prob_grad(const Rows& a, const Cut& k, const ProbOut& out, con
 
 static int launch_prob(const Rows& a, const ProbOut& out, int32_t top, void* workspace,
                        hipStream_t st) {
-    const Cut k = cut_rows(a.type, a.rows, a.vocab);
+    const Cut k = cut_rows(a.type, a.rows, a.vocab, top);
     Part* part = (Part*)workspace;
     uint64_t* lists = (uint64_t*)((char*)workspace + parts_bytes(k, a.rows));
     return by_type(a.type, k.vecs, [&](auto t, auto v) {
@@ -945,7 +956,7 @@ static int launch_prob(const Rows& a, const ProbOut& out, int32_t top, void* wor
 static int launch_prob_both(const Rows& a, const ProbOut& out, void* workspace, const Upstream& g,
                             hipStream_t st) {
     if (launch_rows_prob(a, out, g, st)) return launch_status();
-    const Cut k = cut_rows(a.type, a.rows, a.vocab);
+    const Cut k = cut_rows(a.type, a.rows, a.vocab, 0);
     Part* part = (Part*)workspace;
     const int f = by_type(a.type, k.vecs, [&](auto t, auto v) {
         constexpr int kType = decltype(t)::value, kVecs = decltype(v)::value;
@@ -991,7 +1002,7 @@ static int launch_distill_grad(const Rows& a, const Cut& k, const DistillIn& lis
 // grad null: the forward pass alone
 static int launch_distill(const Rows& a, const DistillIn& list, void* workspace, float* loss,
                           float* stats, const Upstream& g, hipStream_t st) {
-    const Cut k = cut_rows(a.type, a.rows, a.vocab);
+    const Cut k = cut_rows(a.type, a.rows, a.vocab, 0);
     Part* part = (Part*)workspace;
     const int f = by_type(a.type, k.vecs, [&](auto t, auto v) {
         constexpr int kType = decltype(t)::value, kVecs = decltype(v)::value;
@@ -1027,10 +1038,11 @@ size_t flashopt_logprob_workspace_bytes(int32_t type, int64_t rows, int64_t voca
     if (!valid_type(type) || rows < 0 || vocab < 1 || vocab > FLASHOPT_VOCAB_MAX || top < 0 ||
         top > FLASHOPT_TOP_MAX || !rows_fit(type, rows, vocab))
         return 0;
-    const Cut k = cut_rows(type, rows, vocab);
-    if (k.nseg == 1) return 0;
-    const size_t forward = parts_bytes(k, rows) + (size_t)(rows * k.nseg) * (size_t)top * sizeof(uint64_t);
-    return forward > both_bytes(k, rows) ? forward : both_bytes(k, rows);
+    // the forward call's and, so that one workspace serves both, the gradient's
+    const Cut k = cut_rows(type, rows, vocab, top);
+    const size_t lists = k.nseg == 1 ? 0 : (size_t)(rows * k.nseg) * (size_t)top * sizeof(uint64_t);
+    const size_t forward = parts_bytes(k, rows) + lists, both = both_bytes(cut_rows(type, rows, vocab, 0), rows);
+    return forward > both ? forward : both;
 }
 
 int flashopt_logprob(const void* logits, int32_t type, int64_t rows, int64_t vocab,
@@ -1068,7 +1080,7 @@ int flashopt_logprob_backward(const void* logits, int32_t type, int64_t rows, in
     const int g = check_grad(logits, type, rows, vocab, stride, grad, grad_stride);
     if (g) return g;
     return launch_prob_grad({logits, type, rows, vocab, stride, temperature},
-                            cut_rows(type, rows, vocab),
+                            cut_rows(type, rows, vocab, 0),
                             {targets, nullptr, nullptr, nullptr, nullptr, nullptr}, nullptr, stats,
                             {grad_logprob, grad_entropy, grad, grad_stride}, (hipStream_t)stream);
 }
@@ -1136,7 +1148,7 @@ int flashopt_distill_backward(const void* logits, int32_t type, int64_t rows, in
     const int g = check_grad(logits, type, rows, vocab, stride, grad, grad_stride);
     if (g) return g;
     return launch_distill_grad({logits, type, rows, vocab, stride, temperature},
-                               cut_rows(type, rows, vocab), {top_id, top_logprob, top, 1}, nullptr,
+                               cut_rows(type, rows, vocab, 0), {top_id, top_logprob, top, 1}, nullptr,
                                nullptr, stats, {grad_loss, nullptr, grad, grad_stride},
                                (hipStream_t)stream);
 }

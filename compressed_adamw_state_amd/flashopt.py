@@ -756,13 +756,16 @@ def element_type(t: torch.Tensor) -> int:
 
 def row_stride(t: torch.Tensor) -> int:
     """Row stride of a 2-D tensor whose rows are dense."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2:
         raise ValueError("expected a 2-D tensor with dense rows")
-    if t.shape[0] <= 1:
-        return t.shape[1]
-    if t.stride(0) < t.shape[1]:
+    (rows, cols), (stride, step) = t.shape, t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError("expected a 2-D tensor with dense rows")
+    if rows <= 1:
+        return cols
+    if stride < cols:
         raise ValueError("rows overlap: make the tensor contiguous first")
-    return t.stride(0)
+    return stride
 
 
 def _arg(t: Optional[torch.Tensor], dtype, numel: int, device, name: str):
@@ -810,7 +813,8 @@ def _call(fn: str, device, stream, *args) -> None:
 def _logits(logits: torch.Tensor):
     """(address, type, rows, vocab, stride) of 2-D logits."""
     stride = row_stride(logits)
-    return logits.data_ptr(), element_type(logits), logits.shape[0], logits.shape[1], stride
+    rows, vocab = logits.shape
+    return logits.data_ptr(), element_type(logits), rows, vocab, stride
 
 
 def _gradient(grad: torch.Tensor, logits: torch.Tensor):

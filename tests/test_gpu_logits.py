@@ -463,3 +463,14 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for a, b in zip(held, eager):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("words", [512, 1536, 2048, 3584, 4096, 8192])
+def test_rows_at_the_borders_of_the_cut(dtype, words):
+    """Rows that one block takes whole, in short and in long chunks, and the first that it does not."""
+    for over in (0, 1):
+        vocab = words * (4 if dtype == torch.float32 else 8) + over
+        test_logprob_entropy_top(dtype, vocab)
+        test_logprob_gradient(dtype, vocab)
+        test_distill(dtype, vocab, over == 0)
