@@ -89,6 +89,11 @@ struct Segment {
             }
         }
     }
+    // words from the i-th on are past the segment (equal for the block's threads)
+    template <int kVecs>
+    __device__ __forceinline__ bool none(int64_t chunk, int i) const {
+        return begin + chunk * (kVecs * kThreads) + i * kThreads >= end;
+    }
     // a chunk of whole words, all of the segment (equal for the block's threads)
     template <int kVecs>
     __device__ __forceinline__ bool whole(int64_t v0) const {
@@ -471,6 +476,7 @@ __device__ __forceinline__ void grad_words(const Segment<kType, kThreads>& seg, 
         seg.template load<kVecs, true>(ch, r);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
+            if (seg.template none<kVecs>(ch, i)) break;          // 501 x 50257 FP16: 35.5 us for 36.7
             float o[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = k.template value<kFast>(Elem<kType>::get(r[i], e));
@@ -574,7 +580,16 @@ __device__ __forceinline__ Part segment_part(const Segment<kType, kThreads>& seg
 #pragma unroll
             for (int i = 0; i < kVecs; ++i)
                 leave_out<kType>(r[i], marks, ((ch * kVecs + i) * kThreads + (int)threadIdx.x) * Elem<kType>::kE);
-        const float top = sums.template add<kVecs>(r);
+        // A last chunk that is not half full: two words at a time, those there are
+        // (1000 x 50257 BF16: 23.5 us for 27.0; 4000 x 14000, 7/8 full: 27.4 for 26.9).
+        float top = -INFINITY;
+        if (kVecs == kShort || !seg.template none<kVecs>(ch, kVecs / 2)) {
+            top = sums.template add<kVecs>(r);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVecs; i += 2)
+                if (!seg.template none<kVecs>(ch, i)) top = fmaxf(top, sums.template add<2>(r + i));
+        }
         if (kTop) {
             chunk_best[ch * kThreads + threadIdx.x] = top;
             mine = fmaxf(mine, top);
@@ -785,10 +800,9 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(RowsIn<kType> in, 
 // and 15.3; of 65536: 6.1 and 7.6, with the gradient 7.9 and 13.2.  Top entries cost a
 // cut row more: 32 rows of 50257, top 20: 16.3 and 14.4, 21.6 and 17.4; of 128256: 13.0
 // and 17.6.  Longer rows, if few, are cut until kBlocksWanted blocks run (at most
-// kMaxSegments a row, which one wave joins): 501 rows of 50257 in BF16 with the top
-// 20: 33 us whole, 38 us in two or three segments; 128 rows: 26 us in two
-// segments, 23 in eight.  A segment is at most kMaxChunks chunks, whose maxima or
-// marks lie in LDS.
+// kMaxSegments a row, which one wave joins): 128256 entries with their gradient,
+// one row: 6.7 us cut, 23.7 whole; 100 rows: 19.8 and 27.9; 200 rows: 32.1 and 33.7.  A
+// segment is at most kMaxChunks chunks, whose maxima or marks lie in LDS.
 //
 // Chunks are the short ones where there are few of them, or where the last long
 // one of a row that is one or two would be less than 3/4 full: 32 rows of 8000 in
