@@ -796,8 +796,8 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(RowsIn<kType> in, 
 // and for rows of up to kWholeWords words: a launch takes 4 us of host time and the
 // join 3 us of the GPU's.  Measured, the GPU's time of a graph's call, cut and
 // whole, and a call's from the host: 32 rows of 16000 in BF16: 5.7 and 4.9 us, 16.4
-// and 12.5; of 32000: 5.8 and 6.7, 16.4 and 12.5, with the gradient 6.9 and 10.5, 19.3
-// and 15.3; of 65536: 6.1 and 7.6, with the gradient 7.9 and 13.2.  Top entries cost a
+// and 12.5; of 32000: 5.8 and 6.7, 16.4 and 12.5, a distillation's gradient 9.3 and
+// 13.0, 18.1 and 14.3; of 65536: 6.1 and 7.6, 10.7 and 16.9.  Top entries cost a
 // cut row more: 32 rows of 50257, top 20: 16.3 and 14.4, 21.6 and 17.4; of 128256: 13.0
 // and 17.6.  Longer rows, if few, are cut until kBlocksWanted blocks run (at most
 // kMaxSegments a row, which one wave joins): 128256 entries with their gradient,

@@ -158,9 +158,13 @@ __global__ __launch_bounds__(kWaves * kWave, 4) void row_kernel(RowArgs<kType> a
 
 // ---- host ---------------------------------------------------------------------
 
-// Rows from which a block a row is worth it (128 rows of 32000 in BF16: 18 us,
-// 16 in segments; 256 rows: 17 and 20), and the words that the least columns hold.
-constexpr int64_t kRowsWhole = 256, kWordsLeast = 1024;
+// Rows of up to kWordsShort words are taken here however few they are (one row of
+// 16000 in BF16: 4.8 us of the GPU's time for 7.0 in segments, 64 of 32000: 8.3 for
+// 11.1); longer ones, which the segments' code cuts over more blocks, from
+// kRowsWhole rows on (64 rows of 50257 in BF16: 15.9 us for 10.2, 128: 15.9 for 13.9
+// in two launches, from the host 16.0 for 18.4; 200: 16.2 for 19.3).  The least
+// columns hold kWordsLeast words.
+constexpr int64_t kRowsWhole = 128, kWordsShort = 4096, kWordsLeast = 1024;
 
 template <int kType>
 static RowArgs<kType> row_args(const Rows& a, const Upstream& g) {
@@ -184,7 +188,7 @@ static RowArgs<kType> row_args(const Rows& a, const Upstream& g) {
 template <typename F>
 static bool by_row(const Rows& a, F f) {
     const int64_t words = a.vocab / (a.type == FLASHOPT_FP32 ? 4 : 8);
-    if (a.rows < kRowsWhole || words <= kWordsLeast) return false;
+    if (words <= kWordsLeast || (words > kWordsShort && a.rows < kRowsWhole)) return false;
     int waves = 4;
     if (words > (int64_t)waves * kWave * 16) waves = 8;
     if (words > (int64_t)waves * kWave * 16) return false;

@@ -474,3 +474,19 @@ def test_rows_at_the_borders_of_the_cut(dtype, words):
         test_logprob_entropy_top(dtype, vocab)
         test_logprob_gradient(dtype, vocab)
         test_distill(dtype, vocab, over == 0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,words", [(1, 1025), (1, 4096), (1, 4097), (3, 1024), (127, 4097), (128, 4097), (130, 8192), (130, 8193)])
+def test_gradient_of_few_whole_rows(dtype, rows, words):
+    """Just before and behind the borders of the rows that a block holds in registers; the gradient in
+    the logits' place and elsewhere."""
+    vocab = words * (4 if dtype == torch.float32 else 8) + 3
+    x, t, g = draw(rows, vocab, dtype, rows + vocab, True)
+    gl, gh = torch.randn(rows, generator=g), torch.randn(rows, generator=g)
+    ref, tol = P.logprob_grad(x.cuda(), t.cuda(), gl.cuda(), gh.cuda(), 1.0)
+    r = L.token_logprobs_grad(x.cuda(), t.cuda(), gl.cuda(), gh.cuda())
+    near(r.grad, ref, tol, dtype)
+    b = x.cuda()
+    r2 = L.token_logprobs_grad(b, t.cuda(), gl.cuda(), gh.cuda(), inplace=True)
+    assert torch.equal(b, r.grad) and torch.equal(r2.logprob, r.logprob) and torch.equal(r2.entropy, r.entropy)
