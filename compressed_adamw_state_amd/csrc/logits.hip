@@ -2,24 +2,27 @@
 // with entropy and top alternatives, distillation from a teacher's top
 // logits, and their gradients.
 //
-// Mathematics.  With c = log2(e) / T and any shift m, a row's distribution is
-// p_j = 2^((x_j - m) c) / S, S = sum_j 2^((x_j - m) c).  A thread sums, over its
-// words of a segment of a row, with a shift of its own,
+// Mathematics.  With c = log2(e) / T and m the row's largest entry, its
+// distribution is p_j = 2^((x_j - m) c) / S, S = sum_j 2^((x_j - m) c).  A thread
+// sums, over its words of a segment of a row, relative to its own largest entry,
 //   S = sum_j e_j,  U = sum_j e_j d_j   (d_j = (x_j - m) c, e_j = 2^d_j);
-// joining threads, waves and segments rescales them to one shift:
-//   S = sum S_k 2^(D_k),  U = sum 2^(D_k) (U_k + D_k S_k),  D_k = (m_k - m) c.
-// Then log2 p_j = d_j - log2 S and H = ln2 (log2 S - U / S), both without
-// cancellation.
+// joining chunks, threads, waves and segments rescales them to the larger one's:
+//   S = sum S_k 2^(D_k),  U = sum 2^(D_k) (U_k + D_k S_k),  D_k = (m_k - m) c <= 0.
+// Then log2 p_j = d_j - log2 S and H = ln2 (log2 S - U / S).  With m the largest
+// entry S is at least 1 and U at most 0: no sum cancels, and where one token is
+// nearly certain all of log2 S, U / S and its d are as small as the result.  (A
+// shift that lies k bits lower leaves differences of numbers near k there.)
 //
 // The gradients are elementwise in the row's numbers: one more pass over the
 // words, plus a few entries (the given token, the teacher's alternatives) that
 // the block writes again after its dense pass, from logits it read before it, so
 // that a gradient may replace its logits.
 //
-// Rows of BF16 bring 8.5 issue slots an entry (unpack, maximum of two, fma, exp2
-// at a quarter of the rate, two sums) for 2 bytes: 65 us at 2048 x 128256 where
-// HBM takes 97, so the forward pass is bound by HBM (2048 x 128256 BF16: 97 us,
-// 5.4 TB/s; with the 64 best entries 124).
+// Rows of BF16 bring 10.5 issue slots an entry (half for the maximum, of packed
+// pairs; unpack, subtract, multiply, exp2 at a quarter of the rate, bound, two
+// sums) for 2 bytes: 80 us at 2048 x 128256 where HBM takes 97, so the forward pass
+// is bound by HBM with some blocks a CU (2048 x 128256 BF16: 98 us, 5.4 TB/s; with
+// the 64 best entries 125) and by the sums with one (300 x 131072: 24).
 #include <cmath>
 
 #include "logits.hpp"
@@ -282,6 +285,58 @@ __device__ __forceinline__ void segment_top(const Segment<kType>& seg, const flo
 
 // ---- sums ---------------------------------------------------------------------------
 
+// S and U of N words relative to m, S by pairs: a sum that holds the 1 of the
+// row's largest entry loses up to 2^-24 with each small one added to it.
+template <int kType, bool kU, int N>
+__device__ __forceinline__ void word_sums(const u32x4* r, float m, float c, float& s, float& u) {
+    constexpr int E = Elem<kType>::kE;
+    PairSum words;
+    u = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        PairSum word;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float d = (Elem<kType>::get(r[i], e) - m) * c, p = exp2_hw(d);
+            word.add(e, p);
+            // where p is 0 the bound keeps 0 * -inf out of the sum
+            if (kU) u = __builtin_fmaf(p, fmaxf(d, -200.0f), u);
+        }
+        words.add(i, word.total(E));
+        __builtin_amdgcn_sched_barrier(0);       // a word's values at a time in registers
+    }
+    s = words.total(N);
+}
+
+// A thread's running sums of its words, relative to the largest of its entries
+// so far.  The maximum of a chunk's words comes first: against a shift that earlier
+// words fixed, raised when later ones exceed it, this costs 1.3 times the issue
+// slots and no registers (2048 x 128256 BF16 98 us for 98, 300 x 131072 24 for 21).
+template <int kType, bool kU>
+struct Sums {
+    float m, s, u, c;
+    __device__ __forceinline__ explicit Sums(float c_)
+        : m(-INFINITY), s(0.0f), u(0.0f), c(c_) {}
+
+    // N words; returns their maximum
+    template <int N>
+    __device__ __forceinline__ float add(const u32x4* r) {
+        const float top = largest<kType, N>(r);
+        const float m_new = fmaxf(m, top);
+        // -inf: nothing yet, every p is 0
+        const float base = m_new == -INFINITY ? 0.0f : m_new;
+        float cs, cu;
+        word_sums<kType, kU, N>(r, base, c, cs, cu);
+        const float D = fmaxf((m - m_new) * c, -200.0f), f = exp2_hw(D);
+        if (kU) u = f * (u + D * s) + cu;
+        s = s * f + cs;
+        m = m_new;
+        return top;
+    }
+};
+
+// ---- gradients ------------------------------------------------------------------------
+
 // 2^((x - m) c - a) for many x: one fma and one exp2 where m c is small
 // enough, (x - m) formed first where it is not (beyond 2^20 the rounding of
 // m c, at most 2^-24 of it, would no longer be small as an exponent; entries
@@ -302,110 +357,7 @@ struct Shift {
     }
 };
 
-// S and U of N words relative to a shift that was chosen before them, and
-// their maximum (kTop).
-template <int kType, bool kU, bool kTop, bool kBound, int N>
-__device__ __forceinline__ void word_sums(const u32x4* r, const Shift& h, float& s, float& u,
-                                          float& top) {
-    constexpr int E = Elem<kType>::kE;
-    s = 0.0f;
-    u = 0.0f;
-    top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float x = Elem<kType>::get(r[i], e);
-            if (kTop) top = fmaxf(top, x);
-            const float d = h.exponent<true>(x);
-            const float p = exp2_hw(d);
-            s += p;
-            // where p is 0 the bound keeps 0 * -inf out of the sum
-            if (kU) u = __builtin_fmaf(p, kBound ? fmaxf(d, -200.0f) : d, u);
-        }
-        __builtin_amdgcn_sched_barrier(0);       // a word's values at a time in registers
-    }
-}
-
-// A thread's running sums of its words.  The shift m is the maximum of the
-// first words that had one, so that later words need one pass only (a sum may
-// lie on either side of 1); it is raised when words exceed it by 2^24.  Words
-// of -inf alone, NaN, infinities and magnitudes beyond Shift's take the path
-// with a maximum of their own.
-template <int kType, bool kU, bool kTop>
-struct Sums {
-    float m, s, u, c, g;
-    bool bound;                                  // an entry of -inf was seen
-    Shift h;
-    __device__ __forceinline__ explicit Sums(float c_)
-        : m(-INFINITY), s(0.0f), u(0.0f), c(c_), g(1.0f), bound(false), h(-INFINITY, c_, 0.0f) {
-        h.fast = false;
-    }
-
-    // N words; returns their maximum (kTop)
-    template <int N>
-    __device__ __forceinline__ float add(u32x4* r) {
-        float top = -INFINITY;
-        if (h.fast) {
-            float cs, cu;
-            if (!kU || !bound) word_sums<kType, kU, kTop, false, N>(r, h, cs, cu, top);
-            if (kU && (bound || cu != cu)) {
-                bound = true;
-                hide<N>(r);
-                word_sums<kType, kU, kTop, true, N>(r, h, cs, cu, top);
-            }
-            if (cs < 0x1p24f) {
-                if (kU) u = __builtin_fmaf(g, cu - h.left * cs, u);
-                s = __builtin_fmaf(g, cs, s);
-                return top;
-            }
-        }
-        return slow<N>(r);
-    }
-
-    // keeps the compiler from holding a word's unpacked values for a later pass
-    template <int N> static __device__ __forceinline__ void hide(u32x4* r) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) asm volatile("" : "+v"(r[i]));
-    }
-    template <int N>
-    __device__ __forceinline__ float slow(u32x4* r) {
-        constexpr int E = Elem<kType>::kE;
-        hide<N>(r);
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int e = 0; e < E; ++e) top = fmaxf(top, Elem<kType>::get(r[i], e));
-        hide<N>(r);
-        const float m_new = fmaxf(m, top);
-        // -inf: nothing yet, every p is 0
-        const float base = m_new == -INFINITY ? 0.0f : m_new;
-        float cs = 0.0f, cu = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float d = (Elem<kType>::get(r[i], e) - base) * c;
-                const float p = exp2_hw(d);
-                cs += p;
-                if (kU) cu = __builtin_fmaf(p, fmaxf(d, -200.0f), cu);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        const float D = fmaxf((m - m_new) * c, -200.0f), f = exp2_hw(D);
-        if (kU) u = f * (u + D * s) + cu;
-        s = s * f + cs;
-        m = m_new;
-        h = Shift(m, c, 0.0f);
-        g = exp2_hw(-h.left);
-        return top;
-    }
-};
-
-// ---- gradients ------------------------------------------------------------------------
-
-// grad_j = p_j (A + B d_j) with d_j = log2 p_j, plus gl at the given token.
+// grad_j = p_j (A + B d_j) with d_j = log2 p_j; given_grad at the given token.
 template <int kType>
 struct ProbGrad {
     const float *grad_logprob, *grad_entropy;    // either may be null
@@ -416,10 +368,9 @@ struct ProbGrad {
 template <bool kEntropy>
 struct ProbCoef {
     Shift h;
-    float A, B, gl, low;
-    __device__ __forceinline__ ProbCoef(const ProbStats& st, float c, float gl_, float gh)
-        : h(st.m, c, st.l2s), gl(gl_) {
-        if (st.on == 0.0f) gh = 0.0f;            // whatever the upstream gradient
+    float A, B, gl, gh, low;
+    __device__ __forceinline__ ProbCoef(const ProbStats& st, float c, float gl_, float gh_)
+        : h(st.m, c, st.l2s), gl(gl_), gh(st.on == 0.0f ? 0.0f : gh_) {      // whatever the upstream gradient
         A = -gl - gh * st.entropy;
         B = -gh * kLn2;
         low = -200.0f;
@@ -432,9 +383,6 @@ struct ProbCoef {
     template <bool kFast> __device__ __forceinline__ float value(float x) const {
         const float d = h.exponent<kFast>(x);
         return exp2_hw(d) * (kEntropy ? __builtin_fmaf(B, fmaxf(d, low), A) : A);
-    }
-    __device__ __forceinline__ float at_given(float x) const {
-        return (h.fast ? value<true>(x) : value<false>(x)) + gl;
     }
 };
 template <int kType, bool kEntropy>
@@ -501,7 +449,7 @@ __device__ __forceinline__ void prob_grad_segment(const Segment<kType>& seg, flo
     const auto k = prob_coef<kType, kEntropy>(st, c, G, seg.row, t.id >= 0);
     grad_segment<kType, kVecs>(seg, k, g);
     if (threadIdx.x == 0 && t.id >= seg.first_id() && t.id < seg.end_id())
-        g[t.id] = Elem<kType>::down(k.at_given(t.x));
+        g[t.id] = Elem<kType>::down(given_grad<kEntropy>(t.x, st, c, k.gl, k.gh));
 }
 
 template <int kType, int kVecs>
@@ -561,9 +509,8 @@ __device__ __forceinline__ void leave_out(u32x4& r, const uint32_t* marks, int a
     }
 }
 
-// The part of a segment: each thread runs over its words with a maximum of its
-// own, rescaling what it has when a chunk raises it; the threads join at the
-// end.  Every wave gets it.  kListed: `marks` has a bit set for each entry to
+// The part of a segment: each thread runs over its words, relative to its largest
+// entry so far, and the threads join at the end.  Every wave gets it.  kListed: `marks` has a bit set for each entry to
 // leave out.  kTop: the threads' largest entry of each chunk goes to
 // chunk_best, `mine` is its largest of all.
 template <int kType, int kVecs, bool kListed, bool kTop, int kThreads>
@@ -571,7 +518,7 @@ __device__ __forceinline__ Part segment_part(const Segment<kType, kThreads>& seg
                                              const uint32_t* marks, float* chunk_best, Part* red,
                                              float& mine) {
     const int n = seg.template chunks<kVecs>();
-    Sums<kType, !kListed, kTop> sums(c);
+    Sums<kType, !kListed> sums(c);
     mine = -INFINITY;
     for (int ch = 0; ch < n; ++ch) {
         u32x4 r[kVecs];

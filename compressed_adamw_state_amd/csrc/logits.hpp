@@ -11,6 +11,70 @@ struct Part {
     float m, s, u, pad;
 };
 
+// The largest entry of N words.  16-bit types are compared as pairs of integers:
+// those order like the numbers where one is not negative, and against them where
+// all are.  (NaN and infinities of either sign may be the result where the words
+// hold a NaN.)  2 slots a pair of entries less than unpacked.
+template <int kType, int N>
+__device__ __forceinline__ float largest(const u32x4* r) {
+    if constexpr (kType == FLASHOPT_FP32) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m = fmaxf(m, as_f32(r[i][e]));
+        return m;
+    } else {
+        typedef int16_t I2 __attribute__((ext_vector_type(2)));
+        typedef uint16_t U2 __attribute__((ext_vector_type(2)));
+        const uint32_t first = r[0][0];          // (__builtin_bit_cast takes no element of a vector)
+        I2 a = __builtin_bit_cast(I2, first);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t w = r[i][q];
+                a = __builtin_elementwise_max(a, __builtin_bit_cast(I2, w));
+            }
+        int top = max((int)a[0], (int)a[1]);
+        if (top < 0) {
+            U2 b = __builtin_bit_cast(U2, first);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t w = r[i][q];
+                    b = __builtin_elementwise_min(b, __builtin_bit_cast(U2, w));
+                }
+            top = min((int)b[0], (int)b[1]);
+        }
+        return Elem<kType>::up((uint16_t)top);
+    }
+}
+
+// A sum of up to 16 numbers by pairs, pairs of pairs and so on; i counts them, as
+// an unrolled loop's constant.
+struct PairSum {
+    float level[5];
+    __device__ __forceinline__ void add(int i, float x) {
+        int k = 0;
+#pragma unroll
+        for (; k < 4 && (i >> k & 1); ++k) x = level[k] + x;
+        level[k] = x;
+    }
+    __device__ __forceinline__ float total(int n) const {
+        float x = 0.0f;
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < 5; ++k)
+            if (n >> k & 1) {
+                x = any ? level[k] + x : level[k];
+                any = true;
+            }
+        return x;
+    }
+};
+
 // ---- parts --------------------------------------------------------------------------
 
 // The parts of a wave's threads as one (every lane gets it).
@@ -86,6 +150,26 @@ __device__ __forceinline__ Given given_token(const typename Elem<kType>::T* x, i
     if (g.id < 0 || g.id >= vocab) g.id = -1;
     else g.x = Elem<kType>::up(x[g.id]);
     return g;
+}
+
+// The given token's gradient gl (1 - p) - gh p (log p + H), with 1 - p from its
+// logarithm: p itself is near 1 where it matters.
+template <bool kEntropy>
+__device__ __forceinline__ float given_grad(float x, const ProbStats& st, float c, float gl, float gh) {
+    const float d = (x - st.m) * c - st.l2s, y = d * kLn2, p = exp2_hw(d);
+    float rest = 1.0f - p;
+    if (y > -0.25f) {                            // -(e^y - 1): the next term is below 2^-29 of it
+        float t = __builtin_fmaf(y, 1.0f / 7, 1.0f);
+        t = __builtin_fmaf(y * (1.0f / 6), t, 1.0f);
+        t = __builtin_fmaf(y * (1.0f / 5), t, 1.0f);
+        t = __builtin_fmaf(y * (1.0f / 4), t, 1.0f);
+        t = __builtin_fmaf(y * (1.0f / 3), t, 1.0f);
+        t = __builtin_fmaf(y * (1.0f / 2), t, 1.0f);
+        rest = -y * t;
+    }
+    float v = gl * rest;
+    if (kEntropy) v -= gh * (p * (fmaxf(y, -140.0f) + st.entropy));
+    return v;
 }
 
 // one lane

@@ -76,42 +76,27 @@ __global__ __launch_bounds__(kWaves * kWave, 4) void row_kernel(RowArgs<kType> a
         }
         const float z = tid < left ? rest : -INFINITY;
 
-        // A thread's sums, with the maximum of its first words as the shift; if
-        // others exceed it by 2^24, once more with the maximum of all.
-        float m = z, s, u;
-        auto most = [&](int from, int to) {
-#pragma unroll
-            for (int i = 0; i < kCols; ++i)
-                if (i >= from && i < to)
-#pragma unroll
-                    for (int e = 0; e < E; ++e) m = fmaxf(m, Elem<kType>::get(r[i], e));
+        // a thread's sums, relative to its largest entry
+        const float m = fmaxf(z, largest<kType, kCols>(r));
+        const float most = m == -INFINITY ? 0.0f : m;
+        float u = 0.0f;
+        PairSum sum;
+        auto one = [&](float v) {
+            const float d = (v - most) * c, p = exp2_hw(d);
+            u = __builtin_fmaf(p, fmaxf(d, -200.0f), u);
+            return p;
         };
-        auto sums = [&]() {
-            const float base = m == -INFINITY ? 0.0f : m;
-            s = u = 0.0f;
-            auto one = [&](float v) {
-                const float d = (v - base) * c, p = exp2_hw(d);
-                s += p;
-                u = __builtin_fmaf(p, fmaxf(d, -200.0f), u);
-            };
-            one(z);
+        const float first = one(z);
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) {
+        for (int i = 0; i < kCols; ++i) {
+            PairSum word;
 #pragma unroll
-                for (int e = 0; e < E; ++e) one(Elem<kType>::get(r[i], e));
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        };
-        most(0, 2);
-        sums();
-        if (m == -INFINITY || !(s < 0x1p24f)) {
-#pragma unroll
-            for (int i = 0; i < kCols; ++i) asm volatile("" : "+v"(r[i]));
-            most(0, kCols);
-#pragma unroll
-            for (int i = 0; i < kCols; ++i) asm volatile("" : "+v"(r[i]));
-            sums();
+            for (int e = 0; e < E; ++e) word.add(e, one(Elem<kType>::get(r[i], e)));
+            sum.add(i, word.total(E));
+            asm volatile("" : "+v"(r[i]));       // unpacked again for the gradient, not held
+            __builtin_amdgcn_sched_barrier(0);
         }
+        const float s = sum.total(kCols) + first;
         const Part p = wave_part<true>(m, s, u, c);
         if (lane == 0) red[wave] = p;
         __syncthreads();
@@ -149,7 +134,7 @@ __global__ __launch_bounds__(kWaves * kWave, 4) void row_kernel(RowArgs<kType> a
             return p * (kEntropy ? __builtin_fmaf(B, fmaxf(d, -200.0f), A) : A);
         };
         dense(value);
-        if (tid == 0 && t.id >= 0) g[t.id] = Elem<kType>::down(value(t.x) + gl);
+        if (tid == 0 && t.id >= 0) g[t.id] = Elem<kType>::down(given_grad<kEntropy>(t.x, st, c, gl, gh));
         if (!more) break;
         row = next;
         x = nx;
