@@ -727,11 +727,8 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(RowsIn<kType> in, 
                         in.c_low, l, seg.row, loss, nullptr, seg.begin == 0);
     } else {
         st = stats[seg.row];
+        list.tail = st.tail != 0.0f;
         share_list<kType>(seg, in.c, list, l, lr);
-        if (threadIdx.x < kWave && l.id >= 0) {  // q by the forward call's norm
-            const float n = __builtin_rintf(st.norm);
-            l.q = list_q(l, n, st.norm - n, l.q);
-        }
     }
     distill_grad_segment<kType, kVecs>(seg, in.c, st, list.top, l, G);
 }
@@ -1109,7 +1106,7 @@ int flashopt_distill_backward(const void* logits, int32_t type, int64_t rows, in
     const int g = check_grad(logits, type, rows, vocab, stride, grad, grad_stride);
     if (g) return g;
     return launch_distill_grad({logits, type, rows, vocab, stride, temperature},
-                               cut_rows(type, rows, vocab, 0), {top_id, top_logprob, top, 1}, nullptr,
+                               cut_rows(type, rows, vocab, 0), {top_id, top_logprob, top, 0}, nullptr,
                                nullptr, stats, {grad_loss, nullptr, grad, grad_stride},
                                (hipStream_t)stream);
 }

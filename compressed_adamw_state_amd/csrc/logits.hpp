@@ -207,11 +207,13 @@ constexpr float kLog2eLow = 0x1.4ae0cp-26f;      // 1 / log 2 - kLog2e
 struct Listed {
     int id;                                      // -1: none
     float x;                                     // the student's logit
-    float hi, lo;                                // log2 of q before its norm
+    float hi, lo;                                // log2 of q before its norm, from the list's base
     float q;
 };
 // The list's numbers of a row, equal in all lanes: the part of its entries (a
-// repeated id once), Q, the teacher's norm (0 with a tail) as log2.
+// repeated id once), Q, the teacher's norm (0 with a tail) as log2, from the base.
+// Without a tail the base is the whole part of the list's largest number, so that
+// q means the same wherever a list lies; with one it is 0.
 struct ListRow {
     Part part;
     float Q, norm_whole, norm_frac, any;
@@ -219,8 +221,8 @@ struct ListRow {
 
 // q = 2^(hi + lo - norm): whole parts go into the exponent, so that a small q
 // is good to its last bits too
-__device__ __forceinline__ float list_q(const Listed& l, float nwhole, float nfrac, float t) {
-    if (!(l.hi > -300.0f)) return t != t ? t : 0.0f;
+__device__ __forceinline__ float list_q(const Listed& l, float nwhole, float nfrac) {
+    if (l.hi <= -300.0f) return 0.0f;
     const float n = __builtin_rintf(l.hi);
     return __builtin_amdgcn_ldexpf(exp2_hw((l.hi - n) + (l.lo - nfrac)), (int)(n - nwhole));
 }
@@ -248,14 +250,14 @@ __device__ __forceinline__ ListRow list_row(const typename Elem<kType>::T* x, in
     if (!in.tail) {
         const float tm = wave_max(t);
         const float ts = wave_sum(ok ? exp2_hw((t - tm) * kLog2e) : 0.0f);
-        float hi, lo, w, f;
+        float hi, lo, f;
         product_parts(tm, kLog2e, kLog2eLow, hi, lo);
-        log2_parts(ts, w, f);
-        const float n = __builtin_rintf(hi);
-        r.norm_whole = n + w;
-        r.norm_frac = (hi - n) + (lo + f);
+        log2_parts(ts, r.norm_whole, f);
+        const float base = tm == -INFINITY ? 0.0f : __builtin_rintf(hi);     // (nothing but -inf: q = 0)
+        r.norm_frac = (hi - base) + (lo + f);
+        l.hi -= base;
     }
-    l.q = ok ? list_q(l, r.norm_whole, r.norm_frac, t) : 0.0f;
+    l.q = ok ? list_q(l, r.norm_whole, r.norm_frac) : 0.0f;
     r.Q = wave_sum(l.q);
     r.any = __ballot(ok) ? 1.0f : 0.0f;
     return r;
@@ -265,10 +267,10 @@ __device__ __forceinline__ ListRow list_row(const typename Elem<kType>::T* x, in
 //   outside the list: e_j coef, e_j = 2^((x_j - rest_m) c - rest_l2) the
 //                     entry's share of the rest, coef = (Q + r) P - r;
 //   in the list:      (Q + r) p_j - sum of its q, p_j from m and l2s;
-// q from the teacher's log probabilities less norm, all times g / T.  A row
-// without a gradient has on = 0.
+// q from the list again, with its tail or without (1 or 0), all times g / T.  A
+// row without a gradient has on = 0.
 struct DistillStats {
-    float rest_m, rest_l2, coef, qr, m, l2s, norm, on;
+    float rest_m, rest_l2, coef, qr, m, l2s, tail, on;
 };
 
 // The row's numbers from the part of its unlisted entries; `loss`, with each
@@ -308,7 +310,7 @@ __device__ __forceinline__ DistillStats distill_stats(const Part& rest, const Li
         loss = on ? sum * kLn2 : 0.0f;
     }
     return DistillStats{rest_m, rw + rf, on ? (lr.Q + r) * P - r : 0.0f, lr.Q + r, m, sw + sf,
-                        lr.norm_whole + lr.norm_frac, on ? 1.0f : 0.0f};
+                        (float)tail, on ? 1.0f : 0.0f};
 }
 
 // One lane's alternative's gradient (wave 0); w = g / T, 0 where on = 0.
