@@ -86,11 +86,13 @@ def int8_linear(x: torch.Tensor, weight: Int8Weight, bias: Optional[torch.Tensor
         raise ValueError("int8_linear has no gradient: call it under torch.no_grad()")
     if x.device != dev or not x.is_cuda:
         raise ValueError("x and the weight must be on one GPU")
-    shape = x.shape[:-1] + (n,)
-    if out is None:
+    shape, given = x.shape[:-1] + (n,), out is not None
+    if not given:
         out = torch.empty(shape, dtype=x.dtype, device=dev)
     elif out.shape != shape or out.dtype != x.dtype or out.device != dev:
         raise ValueError("out must have x's leading dimensions, type and device, and n features")
+    elif out.requires_grad and torch.is_grad_enabled():
+        raise ValueError("out requires a gradient, which int8_linear does not have")
     if bias is not None and (bias.dtype != x.dtype or bias.shape != (n,) or bias.device != dev
                              or not bias.is_contiguous()):
         raise ValueError("bias must hold n values of x's type on its device")
@@ -103,6 +105,9 @@ def int8_linear(x: torch.Tensor, weight: Int8Weight, bias: Optional[torch.Tensor
             F.row_stride(rows), weight.codes.data_ptr(), weight.scale.data_ptr(),
             None if bias is None else bias.data_ptr(), n, to.data_ptr(), F.row_stride(to),
             None if ws is None else ws.data_ptr(), need)
+    if given:
+        # torch then refuses a backward pass that would read out's former values
+        torch.autograd.graph.increment_version(out)
     return out
 
 
