@@ -158,10 +158,14 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
 def _grad_buffer(logits: torch.Tensor, inplace: bool):
     """(the gradient, its row stride)"""
     if inplace:
-        # torch then refuses a backward pass that would read the logits' values
-        torch.autograd.graph.increment_version(logits)
         return logits.detach(), F.row_stride(_rows(logits))
     return _empty(logits.shape, logits.device, logits.dtype), logits.shape[-1]
+
+
+def _replaced(logits: torch.Tensor, inplace: bool) -> None:
+    """After the call: torch then refuses a backward pass that would read the logits' values."""
+    if inplace:
+        torch.autograd.graph.increment_version(logits)
 
 
 def token_logprobs_grad(logits: torch.Tensor, targets: torch.Tensor, grad_logprob: torch.Tensor,
@@ -185,6 +189,7 @@ def token_logprobs_grad(logits: torch.Tensor, targets: torch.Tensor, grad_logpro
     F._call("flashopt_logprob_grad", dev, None, x, ty, rows, vocab, stride, temperature,
             targets.data_ptr(), grad_logprob.data_ptr(), _at(grad_entropy), _at(ws), need,
             logprob.data_ptr(), entropy.data_ptr(), grad.data_ptr(), grad_stride)
+    _replaced(logits, inplace)
     return TokenLogprobsGrad(logprob, entropy, grad)
 
 
@@ -266,4 +271,5 @@ def distill_grad(logits: torch.Tensor, top_id: torch.Tensor, top_logprob: torch.
     F._call("flashopt_distill_grad", dev, None, x, ty, rows, vocab, stride, temperature,
             top_id.data_ptr(), top_logprob.data_ptr(), top_id.shape[-1], bool(tail),
             grad_loss.data_ptr(), _at(ws), need, loss.data_ptr(), grad.data_ptr(), grad_stride)
+    _replaced(logits, inplace)
     return loss, grad

@@ -6,6 +6,7 @@ import torch
 
 from compressed_adamw_state_amd import flashopt as F
 from compressed_adamw_state_amd import int8 as I
+from compressed_adamw_state_amd import losses as L
 
 pytestmark = pytest.mark.gpu
 
@@ -46,4 +47,16 @@ def test_a_refused_output_stays_as_it_was():
     s = (both * both).sum()
     with pytest.raises(F.FlashoptError):                   # the output lies over the input
         I.int8_linear(both.detach()[:, :200], w, out=both.detach()[:, 150:250])
+    s.backward()
+
+
+def test_a_refused_gradient_in_place_leaves_the_logits_usable():
+    """A vocabulary past the limit: the logits were not replaced, and what saved them still has them."""
+    y = torch.randn(1, F.lib().flashopt_int8_ld(131072) * 4 + 1, device="cuda", requires_grad=True) * 1.0
+    s = (y * y).sum()
+    one, t = torch.ones(1, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
+    with pytest.raises(F.FlashoptError):
+        L.token_logprobs_grad(y, t, one, inplace=True)
+    with pytest.raises(F.FlashoptError):
+        L.distill_grad(y, t.view(1, 1), -one.view(1, 1), one, inplace=True)
     s.backward()
