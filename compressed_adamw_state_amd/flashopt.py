@@ -783,9 +783,11 @@ def _scratch(workspace, need: int, device, stream):
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:               # not to be reused before that stream is done with it
-            workspace.record_stream(stream)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        else:                                # that stream's memory: other streams may still use what they freed
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
     elif workspace.dtype != torch.uint8 or workspace.device != device or \
             not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
