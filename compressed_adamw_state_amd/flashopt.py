@@ -798,6 +798,8 @@ def _call(fn: str, device, stream, *args) -> None:
     """The C call with `device` current, on the stream given or the device's own."""
     if device.type != "cuda":
         raise ValueError("expected device tensors")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is of {stream.device}, the tensors of {device}")
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
             _call(fn, device, stream, *args)

@@ -1,5 +1,5 @@
 """The streams of the language-model operators' calls: a workspace that a call makes for itself is
-memory of the stream that the call runs on."""
+memory of the stream that the call runs on, which is one of the tensors' GPU."""
 import pytest
 import torch
 
@@ -33,6 +33,13 @@ def test_a_calls_own_workspace_is_of_its_stream(monkeypatch):
     assert seen == ["empty"]
     del seen[:]
     assert F._scratch(None, 0, torch.device("cpu"), side) == (None, 0, None) and seen == []
+
+
+def test_a_stream_of_another_gpu_is_refused():
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 0
+    with pytest.raises(ValueError, match="stream"):
+        F._call("flashopt_logprob", torch.device("cuda", 0), Stream())
 
 
 @pytest.mark.gpu
