@@ -15,6 +15,7 @@ from typing import List, Optional, Sequence
 
 import numpy as np
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libflashopt.so")
@@ -752,6 +753,12 @@ def element_type(t: torch.Tensor) -> int:
     if code is None:
         raise ValueError(f"expected BF16, FP16 or FP32, not {t.dtype}")
     return code
+
+
+def no_tangent(t: torch.Tensor, name: str) -> None:
+    """Refuse a tensor of forward-mode differentiation: its results would lack their tangent."""
+    if unpack_dual(t).tangent is not None:
+        raise ValueError(f"{name} has a forward-mode tangent, which this operator does not carry on")
 
 
 def row_stride(t: torch.Tensor) -> int:

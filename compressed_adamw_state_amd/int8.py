@@ -84,6 +84,9 @@ def int8_linear(x: torch.Tensor, weight: Int8Weight, bias: Optional[torch.Tensor
         raise ValueError(f"x has {x.shape[-1]} features, the weight {k}")
     if (x.requires_grad or (bias is not None and bias.requires_grad)) and torch.is_grad_enabled():
         raise ValueError("int8_linear has no gradient: call it under torch.no_grad()")
+    F.no_tangent(x, "x")
+    if bias is not None:
+        F.no_tangent(bias, "bias")
     if x.device != dev or not x.is_cuda:
         raise ValueError("x and the weight must be on one GPU")
     shape, given = x.shape[:-1] + (n,), out is not None

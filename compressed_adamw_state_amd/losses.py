@@ -61,6 +61,7 @@ def _rows(logits: torch.Tensor) -> torch.Tensor:
 def _per_row(t: torch.Tensor, shape, device, dtype, name: str) -> torch.Tensor:
     if t.dtype != dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {device}")
+    F.no_tangent(t, name)
     return t if t.is_contiguous() else t.contiguous()
 
 
@@ -144,6 +145,7 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     the `top` most likely tokens (0 to 64; equal logits by lowest id), of
     softmax(logits / temperature).  logprob and entropy are differentiable."""
     temperature = _check_temperature(temperature)
+    F.no_tangent(logits, "logits")
     if top < 0 or top > F.TOP_MAX or top > logits.shape[-1]:
         raise ValueError(f"top = {top} is outside 0 .. {min(F.TOP_MAX, logits.shape[-1])}")
     lead = logits.shape[:-1]
@@ -176,6 +178,7 @@ def token_logprobs_grad(logits: torch.Tensor, targets: torch.Tensor, grad_logpro
     row).  inplace: the gradient takes the logits' place, whose values nothing
     else may need any more."""
     temperature = _check_temperature(temperature)
+    F.no_tangent(logits, "logits")
     lead, dev = logits.shape[:-1], logits.device
     targets = _per_row(targets, lead, dev, torch.int64, "targets")
     grad_logprob = _per_row(grad_logprob, lead, dev, torch.float32, "grad_logprob")
@@ -247,6 +250,7 @@ def distill_loss(logits: torch.Tensor, top_id: torch.Tensor, top_logprob: torch.
     whole.  Differentiable in the logits; multiply by temperature ** 2 for
     the customary weight."""
     temperature = _check_temperature(temperature)
+    F.no_tangent(logits, "logits")
     lead = logits.shape[:-1]
     top_id, top_logprob = _teacher(logits, lead, top_id, top_logprob)
     if logits.requires_grad and torch.is_grad_enabled():
@@ -260,6 +264,7 @@ def distill_grad(logits: torch.Tensor, top_id: torch.Tensor, top_logprob: torch.
     """(loss, gradient of sum(grad_loss * loss) with respect to the logits);
     grad_loss: FP32, one per row; inplace as in token_logprobs_grad."""
     temperature = _check_temperature(temperature)
+    F.no_tangent(logits, "logits")
     lead, dev = logits.shape[:-1], logits.device
     top_id, top_logprob = _teacher(logits, lead, top_id, top_logprob)
     grad_loss = _per_row(grad_loss, lead, dev, torch.float32, "grad_loss")
