@@ -118,7 +118,7 @@ def _matrix(t: torch.Tensor, cols: int, name: str) -> torch.Tensor:
     if t.dim() == 2:
         return t
     try:
-        return t.view(-1, cols)
+        return t.view(t.shape[:-1].numel(), cols)
     except RuntimeError:
         raise ValueError(f"{name}'s leading dimensions must flatten without a copy") from None
 

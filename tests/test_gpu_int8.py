@@ -223,3 +223,12 @@ def test_linear_of_few_rows_or_channels(dtype, m, n, k):
 def test_linear_of_few_tokens(dtype, m, n, k):
     """Tokens rounded by the product's own blocks of 4 or 8 waves, and just past what those hold."""
     test_linear(dtype, m, n, k)
+
+
+def test_no_outputs():
+    """A layer without output channels, with any leading dimensions."""
+    w = I.Int8Weight.from_weight(torch.zeros(0, 40, device="cuda"))
+    for shape in ((40,), (7, 40), (2, 3, 40), (0, 3, 40)):
+        x = torch.ones(shape, device="cuda")
+        assert I.int8_linear(x, w).shape == shape[:-1] + (0,)
+        assert I.int8_linear(x, w, torch.empty(0, device="cuda")).shape == shape[:-1] + (0,)
