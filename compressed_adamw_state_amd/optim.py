@@ -420,7 +420,7 @@ class _FlashOptimizer(torch.optim.Optimizer):
         self._join_release()
         if p.dim() < 2:
             raise ValueError("export_int8 needs a matrix")
-        return Int8Weight.from_state(self.state[p]["flash"], p.numel() // p.shape[0])
+        return Int8Weight.from_state(self.state[p]["flash"], p.shape[1:].numel())
 
 
 class FlashAdamW(_FlashOptimizer):

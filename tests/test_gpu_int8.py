@@ -232,3 +232,10 @@ def test_no_outputs():
         x = torch.ones(shape, device="cuda")
         assert I.int8_linear(x, w).shape == shape[:-1] + (0,)
         assert I.int8_linear(x, w, torch.empty(0, device="cuda")).shape == shape[:-1] + (0,)
+
+
+def test_export_of_no_rows():
+    p = torch.nn.Parameter(torch.zeros(0, 40, device="cuda"))
+    q = torch.nn.Parameter(torch.ones(3, 40, device="cuda"))
+    w = O.FlashAdamW([p, q], lr=1e-2).export_int8(p)
+    assert (w.n, w.k) == (0, 40) and w.codes.shape == (0, 128)
