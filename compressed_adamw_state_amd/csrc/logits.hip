@@ -71,7 +71,7 @@ struct Segment {
     // kLast: nothing reads these logits after this call's gradient.  With the
     // non-temporal hint here and on the gradient's stores, the rows that other
     // blocks have read once stay in the last-level cache until their gradient:
-    // 4096 x 128256 BF16 distillation takes 491 us, 651 without either hint.
+    // 4096 x 128256 BF16 distillation takes 500 us, 646 without either hint.
     template <int kVecs, bool kLast = false>
     __device__ __forceinline__ void load(int64_t chunk, u32x4* r) const {
         const int64_t v0 = begin + chunk * (kVecs * kThreads);
@@ -424,7 +424,7 @@ __device__ __forceinline__ void grad_words(const Segment<kType, kThreads>& seg, 
         seg.template load<kVecs, true>(ch, r);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            if (seg.template none<kVecs>(ch, i)) break;          // 501 x 50257 FP16: 35.5 us for 36.7
+            if (seg.template none<kVecs>(ch, i)) break;          // 501 x 50257 FP16: 37.1 us for 38.2
             float o[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = k.template value<kFast>(Elem<kType>::get(r[i], e));
@@ -528,7 +528,7 @@ __device__ __forceinline__ Part segment_part(const Segment<kType, kThreads>& seg
             for (int i = 0; i < kVecs; ++i)
                 leave_out<kType>(r[i], marks, ((ch * kVecs + i) * kThreads + (int)threadIdx.x) * Elem<kType>::kE);
         // A last chunk that is not half full: two words at a time, those there are
-        // (1000 x 50257 BF16: 23.5 us for 27.0; 4000 x 14000, 7/8 full: 27.4 for 26.9).
+        // (1000 x 50257 BF16: 25.4 us for 27.8; 4000 x 14000, 7/8 full: 26.0 for 26.0).
         float top = -INFINITY;
         if (kVecs == kShort || !seg.template none<kVecs>(ch, kVecs / 2)) {
             top = sums.template add<kVecs>(r);
@@ -739,18 +739,23 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(RowsIn<kType> in, 
 // whole row (no join, one launch) from kBlocksWanted rows on, a block for each CU,
 // and for rows of up to kWholeWords words: a launch takes 4 us of host time and the
 // join 3 us of the GPU's.  Measured, the GPU's time of a graph's call, cut and
-// whole, and a call's from the host: 32 rows of 16000 in BF16: 5.7 and 4.9 us, 16.4
-// and 12.5; of 32000: 5.8 and 6.7, 16.4 and 12.5, a distillation's gradient 9.3 and
-// 13.0, 18.1 and 14.3; of 65536: 6.1 and 7.6, 10.7 and 16.9.  Top entries cost a
-// cut row more: 32 rows of 50257, top 20: 16.3 and 14.4, 21.6 and 17.4; of 128256: 13.0
-// and 17.6.  Longer rows, if few, are cut until kBlocksWanted blocks run (at most
-// kMaxSegments a row, which one wave joins): 128256 entries with their gradient,
-// one row: 6.7 us cut, 23.7 whole; 100 rows: 19.8 and 27.9; 200 rows: 32.1 and 33.7.  A
-// segment is at most kMaxChunks chunks, whose maxima or marks lie in LDS.
+// whole, and a call's from the host: 32 rows of 16000 in BF16: 6.1 and 5.2 us, 17.3
+// and 13.4; of 32000: 6.1 and 6.5, 17.2 and 13.4; of 65536: 6.6 and 11.3, 17.1 and
+// 13.3.  At kWholeWords the host's time decides, at the cost of a replayed graph:
+// a distillation's gradient of 32 rows of 32000 takes 9.8 us cut and 14.2 whole, from
+// the host 18.3 and 14.4.  Top entries cost a cut row more: 32 rows of 50257, top 20:
+// 16.8 and 14.2, 22.8 and 19.8; of 128256: 13.4 and 19.2.
+//
+// Longer rows, if few, are cut until 2 kBlocksWanted blocks run, with top entries
+// kBlocksWanted (at most kMaxSegments a row, which one wave joins): 128256 entries
+// with their gradient, one row: 7.0 us cut, 21.5 whole; 100 rows: 19.2 (21.0 with
+// half the blocks) and 30.7; 200 rows: 31.8 (33.1) and 36.8; but 100 rows' 64 best 26.0
+// to 31.7 with twice the blocks or more for 29.6, 20 rows' 45.2 for 42.4.  A segment is
+// at most kMaxChunks chunks, whose maxima or marks lie in LDS.
 //
 // Chunks are the short ones where there are few of them, or where the last long
 // one of a row that is one or two would be less than 3/4 full: 32 rows of 8000 in
-// BF16: 4.2 us for 4.9, of 24000: 6.0 for 6.8, but of 32000: 6.9 for 6.7.
+// BF16: 4.4 us for 4.8, of 24000 6.4 for 6.2, but of 32000 7.4 for 6.5.
 constexpr int64_t kBlocksWanted = 256, kWholeWords = 4096, kWholeWordsTop = 8192;
 constexpr int kMaxChunks = 16;
 struct Cut {
@@ -767,8 +772,9 @@ static Cut cut_rows(int32_t type, int64_t rows, int64_t vocab, int32_t top) {
     k.vecs = kLong;
     if (whole ? lng <= 2 && (words - 1) % step_long < step_long * 3 / 4 : rows * lng < 256) k.vecs = kShort;
     const int64_t step = (int64_t)k.vecs * kBlock, chunks = (words + step - 1) / step;
-    int64_t want = whole ? 1 : (kBlocksWanted + rows - 1) / (rows < 1 ? 1 : rows);
-    want = want < 1 ? 1 : want > kMaxSegments ? kMaxSegments : want;
+    const int64_t blocks = top > 0 ? kBlocksWanted : 2 * kBlocksWanted;
+    int64_t want = whole || rows >= kBlocksWanted ? 1 : (blocks + rows - 1) / (rows < 1 ? 1 : rows);
+    if (want > kMaxSegments) want = kMaxSegments;
     k.chunks = (int)((chunks + want - 1) / want);
     if (k.chunks > kMaxChunks) k.chunks = kMaxChunks;
     k.span = k.chunks * step;

@@ -4,12 +4,12 @@
 // A block keeps a row in its registers, kCols 16-byte words a thread, so that
 // it is read once and its gradient written once; while the gradient of a
 // column of words is stored, the same column of the block's next row is
-// loaded into its place.  Against the segments' code, which reads a row a
-// second time from the last-level cache: 4096 x 32000 BF16 106 us for 119, 1024 x
-// 50257 BF16 52 for 61, 1024 x 50257 FP32 77 for 98 (HBM at the rate of a copy: 102,
+// loaded into its place.  (The last row's loads have no next row: they read that row
+// again and are thrown away.)  Against the segments' code, which reads a row a
+// second time from the last-level cache: 4096 x 32000 BF16 94 us for 121, 1024 x
+// 50257 BF16 50 for 60, 1024 x 50257 FP32 100 for 100 (HBM at the rate of a copy: 102,
 // 40, 80).  Rows that would need a block of 16 waves, alone on its CU, are left to
-// the segments: nothing else runs there between a row's loads and its sums (4096 x
-// 128256 with a list: 672 us for 491).
+// the segments: nothing else runs there between a row's loads and its sums.
 //
 // What keeps the loop free of waits: every load is unconditional (loads and
 // stores come back in order, so a load that a branch may skip would be waited
@@ -144,10 +144,10 @@ __global__ __launch_bounds__(kWaves * kWave, 4) void row_kernel(RowArgs<kType> a
 // ---- host ---------------------------------------------------------------------
 
 // Rows of up to kWordsShort words are taken here however few they are (one row of
-// 16000 in BF16: 4.8 us of the GPU's time for 7.0 in segments, 64 of 32000: 8.3 for
-// 11.1); longer ones, which the segments' code cuts over more blocks, from
-// kRowsWhole rows on (64 rows of 50257 in BF16: 15.9 us for 10.2, 128: 15.9 for 13.9
-// in two launches, from the host 16.0 for 18.4; 200: 16.2 for 19.3).  The least
+// 16000 in BF16: 5.3 us of the GPU's time for 7.4 in segments, 64 of 32000: 8.2 for
+// 11.0); longer ones, which the segments' code cuts over more blocks, from
+// kRowsWhole rows on (64 rows of 50257 in BF16: 16.4 us for 10.7, 128: 16.8 for 13.9
+// in two launches, from the host 17.8 for 20.4; 200: 17.1 for 21.2).  The least
 // columns hold kWordsLeast words.
 constexpr int64_t kRowsWhole = 128, kWordsShort = 4096, kWordsLeast = 1024;
 
