@@ -749,9 +749,9 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(RowsIn<kType> in, 
 // Longer rows, if few, are cut until 2 kBlocksWanted blocks run, with top entries
 // kBlocksWanted (at most kMaxSegments a row, which one wave joins): 128256 entries
 // with their gradient, one row: 7.0 us cut, 21.5 whole; 100 rows: 19.2 (21.0 with
-// half the blocks) and 30.7; 200 rows: 31.8 (33.1) and 36.8; but 100 rows' 64 best 26.0
-// to 31.7 with twice the blocks or more for 29.6, 20 rows' 45.2 for 42.4.  A segment is
-// at most kMaxChunks chunks, whose maxima or marks lie in LDS.
+// half the blocks) and 30.7; 200 rows: 31.8 (33.1) and 36.8; but the 64 best of 64 rows
+// with twice the blocks 27.3 for 21.7, of 250 rows 38.1 for 31.9.  A segment is at most
+// kMaxChunks chunks, whose maxima or marks lie in LDS.
 //
 // Chunks are the short ones where there are few of them, or where the last long
 // one of a row that is one or two would be less than 3/4 full: 32 rows of 8000 in

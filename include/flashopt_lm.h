@@ -37,9 +37,10 @@ typedef enum flashopt_type {
  * aligned to its element type only (rows of an odd vocabulary start
  * anywhere).  With z = x / T (T > 0, the temperature),
  *   m = max_j z_j,  S = sum_j e^(z_j - m),  p_j = e^(z_j - m) / S.
- * An entry of -inf has probability 0 and gradient 0.  A row whose entries are
- * all -inf has no distribution: its entropy and loss are 0, its log
- * probabilities -inf and its gradient 0.  Entries of the type's lowest value
+ * An entry of -inf has probability 0 and, unless it is the given token or a
+ * listed one, gradient 0 (those keep their own term, gl / T or -g q / T).  A row
+ * whose entries are all -inf has no distribution: its entropy and loss are 0, its
+ * log probabilities -inf and its gradient 0.  Entries of the type's lowest value
  * are ordinary numbers.  A NaN or +inf in a row gives NaN in that row's
  * results (its top_id stay in range).  Sums are binary32; a gradient is
  * rounded once, to the logits' type, to nearest even.
@@ -93,7 +94,8 @@ int flashopt_logprob_grad(const void* logits, int32_t type, int64_t rows, int64_
 /* Distillation.  A teacher gives each row `top` token ids and their log
  * probabilities t_k at the same temperature (flashopt_logprob's top_id and
  * top_logprob); 1 <= top.  q_k = e^(t_k) over the ids in range.
- *   tail = 0: q is divided by its sum; loss = sum_k q_k (log q_k - log p_k);
+ *   tail = 0: q is divided by its sum (t may lie anywhere: scores will do);
+ *             loss = sum_k q_k (log q_k - log p_k);
  *   tail = 1: the rest of the vocabulary is one more outcome, with
  *             r = max(0, 1 - sum q) and P = sum of p_j over the ids not
  *             listed: loss += r (log r - log P); where P = 0 (nothing is
@@ -137,8 +139,8 @@ int64_t flashopt_int8_ld(int64_t cols);
 int flashopt_quantize_rows(const void* x, int32_t type, int64_t rows, int64_t cols,
                            int64_t stride, int8_t* codes, float* scale, void* stream);
 /* From one tensor's state (any kind): its master weight theta' + (rho*K8)*h
- * (or the FP32 master weight) as numel / cols rows, rebuilt and rounded in one pass, no
- * FP32 copy.  cols must divide numel. */
+ * (or the FP32 master weight) as numel / cols rows, rebuilt twice (for a row's scale, then
+ * for its codes) without an FP32 copy.  cols must divide numel. */
 int flashopt_tensor_quantize_rows(const flashopt_tensor* t, int32_t kind, int64_t cols,
                                   int8_t* codes, float* scale, void* stream);
 /* out[i][j] = RN_type(a_scale[i] * b_scale[j] * sum_c a[i][c] b[j][c] + bias[j]):
