@@ -357,7 +357,9 @@ struct Shift {
     }
 };
 
-// grad_j = p_j (A + B d_j) with d_j = log2 p_j; given_grad at the given token.
+// grad_j = scale p_j (A + B d_j) with d_j = log2 p_j; given_grad at the given
+// token.  1 / T is the scale, so that A and B do not overflow where the gradient
+// does not; without the entropy it is part of A.
 template <int kType>
 struct ProbGrad {
     const float *grad_logprob, *grad_entropy;    // either may be null
@@ -368,9 +370,10 @@ struct ProbGrad {
 template <bool kEntropy>
 struct ProbCoef {
     Shift h;
-    float A, B, gl, gh, low;
-    __device__ __forceinline__ ProbCoef(const ProbStats& st, float c, float gl_, float gh_)
-        : h(st.m, c, st.l2s), gl(gl_), gh(st.on == 0.0f ? 0.0f : gh_) {      // whatever the upstream gradient
+    float A, B, gl, gh, scale, low;
+    __device__ __forceinline__ ProbCoef(const ProbStats& st, float c, float gl_, float gh_, float inv_t)
+        : h(st.m, c, st.l2s), gl(kEntropy ? gl_ : gl_ * inv_t),
+          gh(st.on == 0.0f ? 0.0f : gh_), scale(inv_t) {         // whatever the upstream gradient
         A = -gl - gh * st.entropy;
         B = -gh * kLn2;
         low = -200.0f;
@@ -381,16 +384,20 @@ struct ProbCoef {
         }
     }
     template <bool kFast> __device__ __forceinline__ float value(float x) const {
-        const float d = h.exponent<kFast>(x);
-        return exp2_hw(d) * (kEntropy ? __builtin_fmaf(B, fmaxf(d, low), A) : A);
+        const float d = h.exponent<kFast>(x), p = exp2_hw(d);
+        return kEntropy ? p * __builtin_fmaf(B, fmaxf(d, low), A) * scale : p * A;
+    }
+    __device__ __forceinline__ float at_given(float x, const ProbStats& st) const {
+        const float v = given_grad<kEntropy>(x, st, h.c, gl, gh);
+        return kEntropy ? v * scale : v;
     }
 };
 template <int kType, bool kEntropy>
 __device__ __forceinline__ ProbCoef<kEntropy> prob_coef(const ProbStats& st, float c,
                                                         const ProbGrad<kType>& G, int64_t row,
                                                         bool given) {
-    const float gl = given && st.on != 0.0f && G.grad_logprob ? G.grad_logprob[row] * G.inv_t : 0.0f;
-    return ProbCoef<kEntropy>(st, c, gl, kEntropy ? G.grad_entropy[row] * G.inv_t : 0.0f);
+    const float gl = given && st.on != 0.0f && G.grad_logprob ? G.grad_logprob[row] : 0.0f;
+    return ProbCoef<kEntropy>(st, c, gl, kEntropy ? G.grad_entropy[row] : 0.0f, G.inv_t);
 }
 
 template <int kType>
@@ -449,7 +456,7 @@ __device__ __forceinline__ void prob_grad_segment(const Segment<kType>& seg, flo
     const auto k = prob_coef<kType, kEntropy>(st, c, G, seg.row, t.id >= 0);
     grad_segment<kType, kVecs>(seg, k, g);
     if (threadIdx.x == 0 && t.id >= seg.first_id() && t.id < seg.end_id())
-        g[t.id] = Elem<kType>::down(given_grad<kEntropy>(t.x, st, c, k.gl, k.gh));
+        g[t.id] = Elem<kType>::down(k.at_given(t.x, st));
 }
 
 template <int kType, int kVecs>

@@ -126,15 +126,18 @@ __global__ __launch_bounds__(kWaves * kWave, 4) void row_kernel(RowArgs<kType> a
         };
         const ProbStats st = prob_stats(all);
         if (tid == 0) write_prob(row, c, st, t, a.out);
-        const float gl = t.id >= 0 && st.on != 0.0f && a.up ? a.up[row] * a.inv_t : 0.0f;
-        const float gh = kEntropy && st.on != 0.0f ? a.up_entropy[row] * a.inv_t : 0.0f;
+        // 1 / T comes last (without the entropy: in A), so that nothing overflows before
+        const float last = kEntropy ? a.inv_t : 1.0f, first_t = kEntropy ? 1.0f : a.inv_t;
+        const float gl = t.id >= 0 && st.on != 0.0f && a.up ? a.up[row] * first_t : 0.0f;
+        const float gh = kEntropy && st.on != 0.0f ? a.up_entropy[row] : 0.0f;
         const float A = -gl - gh * st.entropy, B = -gh * kLn2, base = st.m, l2 = st.l2s;
         auto value = [&](float v) {
             const float d = __builtin_fmaf(v - base, c, -l2), p = exp2_hw(d);
-            return p * (kEntropy ? __builtin_fmaf(B, fmaxf(d, -200.0f), A) : A);
+            return kEntropy ? p * __builtin_fmaf(B, fmaxf(d, -200.0f), A) * last : p * A;
         };
         dense(value);
-        if (tid == 0 && t.id >= 0) g[t.id] = Elem<kType>::down(given_grad<kEntropy>(t.x, st, c, gl, gh));
+        if (tid == 0 && t.id >= 0)
+            g[t.id] = Elem<kType>::down(given_grad<kEntropy>(t.x, st, c, gl, gh) * last);
         if (!more) break;
         row = next;
         x = nx;
