@@ -43,7 +43,8 @@ typedef enum flashopt_type {
  * log probabilities -inf and its gradient 0.  Entries of the type's lowest value
  * are ordinary numbers.  A NaN or +inf in a row gives NaN in that row's
  * results (its top_id stay in range).  Sums are binary32; a gradient is
- * rounded once, to the logits' type, to nearest even.
+ * rounded once, to the logits' type, to nearest even.  What lies within a factor
+ * of 16 of binary32's largest number (temperatures near 2^-126) may be infinite.
  *
  * A token id outside [0, vocab) stands for none (padding; -100 by custom):
  * its row's log probability is 0 and has no gradient, and a teacher's
