@@ -872,10 +872,10 @@ static int launch_matmul(const Plan& plan, const int8_t* a, const float* a_scale
 // again and again, the GPU's time here and in two launches: 1 token: 4096 x 4096
 // 5.3 and 8.2 us, 14336 x 4096 11.5 and 15.9 (12 weights by turns, which no cache
 // holds: 14.2 and 17.4), 128256 x 4096 87 and 90, 28672 x 8192 40.1 and 40.2, but 50257
-// x 768 (3142 blocks) 17.2 and 12.4 (of 2048: 18.4 and 21.0); 2 tokens, 4096 x 4096: 6.8 and 8.9;
-// 4 tokens, 4096 x 2048: 5.6 and 6.6, 2304 x 768: 5.1 and 6.4.  Blocks of 4 waves leave
-// room for more of them: 1 token, 14336 x 4096: 11.5 us, 14.0 with 8 waves; up to one
-// block a CU 8 waves read faster (4096 x 4096: 5.3 for 6.7).
+// x 768 (3142 blocks) 17.2 and 12.4 (of 2048: 18.4 and 21.0); 2 tokens, 4096 x 4096:
+// 6.8 and 8.9; 4 tokens, 4096 x 2048: 5.6 and 6.6, 2304 x 768: 5.1 and 6.4.  Blocks of 4
+// waves leave room for more of them: 1 token, 14336 x 4096: 11.5 us, 14.0 with 8
+// waves; up to one block a CU 8 waves read faster (4096 x 4096: 5.3 for 6.7).
 static int few_waves(int64_t m, int64_t n, int64_t k) {
     const int64_t blocks = (n + 15) / 16, rows = m <= 1 ? 1 : m <= 2 ? 2 : 4;
     if (m > kFewTokens || k < 8 || (blocks > 1024 && k < 4096)) return 0;

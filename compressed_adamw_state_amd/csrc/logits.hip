@@ -517,9 +517,9 @@ __device__ __forceinline__ void leave_out(u32x4& r, const uint32_t* marks, int a
 }
 
 // The part of a segment: each thread runs over its words, relative to its largest
-// entry so far, and the threads join at the end.  Every wave gets it.  kListed: `marks` has a bit set for each entry to
-// leave out.  kTop: the threads' largest entry of each chunk goes to
-// chunk_best, `mine` is its largest of all.
+// entry so far, and the threads join at the end.  Every wave gets it.  kListed:
+// `marks` has a bit set for each entry to leave out.  kTop: the threads' largest
+// entry of each chunk goes to chunk_best, `mine` is its largest of all.
 template <int kType, int kVecs, bool kListed, bool kTop, int kThreads>
 __device__ __forceinline__ Part segment_part(const Segment<kType, kThreads>& seg, float c,
                                              const uint32_t* marks, float* chunk_best, Part* red,

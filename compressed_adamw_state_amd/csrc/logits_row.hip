@@ -8,8 +8,9 @@
 // again and are thrown away.)  Against the segments' code, which reads a row a
 // second time from the last-level cache: 4096 x 32000 BF16 94 us for 121 over the same
 // logits again and again (105 over four by turns), 1024 x 50257 BF16 50 for 60, 1024 x
-// 50257 FP32 100 for 100 (HBM at the rate of a copy: 102, 40, 80).  Rows that would need a block of 16 waves, alone on its CU, are left to
-// the segments: nothing else runs there between a row's loads and its sums.
+// 50257 FP32 100 for 100 (HBM at the rate of a copy: 102, 40, 80).  Rows that would
+// need a block of 16 waves, alone on its CU, are left to the segments: nothing else
+// runs there between a row's loads and its sums.
 //
 // What keeps the loop free of waits: every load is unconditional (loads and
 // stores come back in order, so a load that a branch may skip would be waited
