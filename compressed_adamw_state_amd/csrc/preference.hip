@@ -132,10 +132,14 @@ __global__ __launch_bounds__(kPairThreads) void preference_kernel(PreferenceIn i
             in.reward[2 * pair] = (float)r[0];
             in.reward[2 * pair + 1] = (float)r[1];
         }
-        // max(0, -d) + log(1 + e^-|d|), where the sum is not NaN
-        if (in.loss)
-            in.loss[pair] = (float)((1.0 - in.smoothing) * ((d > 0.0 ? 0.0 : -d) + low) +
-                                    in.smoothing * ((d > 0.0 ? d : 0.0) + low));
+        // log(1 + e^-d) = max(0, -d) + log(1 + e^-|d|), NaN where d is, and log(1 + e^d); one of
+        // them is infinite where d is, and of weight 0 then not 0 * infinity
+        if (in.loss) {
+            double x = 0.0;
+            if (in.smoothing < 1.0) x = (1.0 - in.smoothing) * ((d > 0.0 ? 0.0 : -d) + low);
+            if (in.smoothing > 0.0) x += in.smoothing * ((d > 0.0 ? d : 0.0) + low);
+            in.loss[pair] = (float)x;
+        }
     }
     if (!in.grad) return;
     // 1 / (1 + e^d) and 1 / (1 + e^-d)

@@ -162,7 +162,10 @@ int flashopt_policy_grad(const void* logits, int32_t type, int64_t rows, int64_t
  * 2 * pairs sequences, pair p the chosen one 2p and the rejected one 2p + 1.  With
  *   r_i = beta sum (logprob - ref_logprob) over its tokens (divided by their number
  *         where `average`; 0 for none), d = r_2p - r_(2p+1) - margin,
- *   loss_p = (1 - smoothing) log(1 + e^-d) + smoothing log(1 + e^d).
+ *   loss_p = (1 - smoothing) log(1 + e^-d) + smoothing log(1 + e^d),
+ * a term of weight 0 left out.  Where d is infinite (one sequence is impossible, itself
+ * or by the reference) loss and gradient have their limits; where it is NaN (both
+ * are) so are they.
  * reward: 2 * pairs, the r_i.  grad_logprob: the gradient of
  * sum_p grad_loss[p] * loss[p] (NULL: 1), one for each of `tokens`, 0 for tokens
  * of no sequence.  A token with mask[t] = 0 does not count, whatever its numbers
