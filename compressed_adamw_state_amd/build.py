@@ -26,7 +26,7 @@ UNITS = ["step.hip", "step_fp32.hip", "tensor.hip", "ablation.hip", "probe.hip",
          "preference.hip", "activations.hip", "weight_grad.hip", "embedding.hip"]
 SOURCES = [os.path.join(CSRC, u) for u in UNITS] + [
     os.path.join(CSRC, h) for h in ("codec.hpp", "device.hpp", "host.hpp", "quant.hpp", "rows.hpp", "logits.hpp",
-                              "policy.hpp", "held.hpp")]
+                              "policy.hpp", "held.hpp", "grad_plan.hpp")]
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libflashopt.so")
 ARCH = os.environ.get("FLASHOPT_ARCH", "gfx950")
@@ -43,6 +43,22 @@ FLAGS = [
 
 TEST_SRC = os.path.join(ROOT, "tests", "hip", "codec_exhaustive.hip")
 TEST_LIB = os.path.join(ROOT, "tests", "hip", "libcodec_exhaustive.so")
+
+
+PLAN_SRC = os.path.join(ROOT, "tests", "hip", "weight_grad_plan.cpp")
+PLAN_LIB = os.path.join(ROOT, "tests", "hip", "libweight_grad_plan.so")
+
+
+def build_plan_lib(verbose: bool = False) -> str:
+    """Which way a weight gradient is done, for the tests to ask (host code)."""
+    tmp = PLAN_LIB + ".tmp"
+    cmd = ["g++", "-O1", "-std=c++17", "-Wall", "-shared", "-fPIC", "-I", os.path.join(ROOT, "include"),
+           "-I", CSRC, "-o", tmp, PLAN_SRC]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, PLAN_LIB)
+    return PLAN_LIB
 
 
 def build_test_lib(verbose: bool = False) -> str:
