@@ -1,6 +1,7 @@
 """What a layer keeps between its forward and its backward pass, held in 8 bits:
 codes with a power of two for each 32 values of a row (include/flashopt_lm.h),
-8.25 bits a value, each off by at most 1/127 of its group's largest magnitude.
+8.25 bits a value, each off by at most 1/127 of its group's largest magnitude
+(by 2^-127 where that is below 2^-120).
 
 * linear: a linear layer that keeps its input in 8 bits; its weight's gradient
   comes from the codes, which enter the matrix instructions exactly;

@@ -245,8 +245,10 @@ int flashopt_int8_linear(const void* x, int32_t type, int64_t m, int64_t k, int6
  * a = max |x| holds e, the least exponent with rne(a 2^-e) <= 127, and
  *   q = rne(x 2^-e) in [-127, 127],  value = q 2^e,  byte = e + 127,
  * with -126 <= e <= 121 (FP16: -24 <= e <= 9; at the upper bound q is limited to 127).  So a
- * value is off by at most 2^(e-1), 1/127 of the group's largest magnitude, and is
- * exact in the input's type and in BF16.  A group that holds an
+ * value is off by at most 2^(e-1), or, where q is limited (FP16 beyond 65280, FP32 beyond
+ * 255 * 2^120), by less than 2^e; in either case by at most 1/127 of the group's largest
+ * magnitude, unless that is below 2^-120, where e = -126 and it is off by up to 2^-127 (FP16 at
+ * e = -24 by nothing).  It is exact in the input's type and in BF16.  A group that holds an
  * infinity or NaN has codes 0 and byte 255: its values read as NaN.  Padding holds
  * zeros.  Codes are 16-byte aligned.
  * Limits: rows <= 2^24, 1 <= cols <= FLASHOPT_INT8_COLS_MAX. */
