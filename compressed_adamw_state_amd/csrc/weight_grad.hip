@@ -6,7 +6,9 @@
 // take both factors exactly and sum in binary32.  A binary32 dy is three BF16
 // numbers, its upper 8 bits, the next 8 and the last 8 (by truncation, so none
 // overflows): three products in place of one, against the binary32 matrix
-// instructions' 1/16 of the rate.
+// instructions' 1/16 of the rate.  BF16's smallest step is 2^-133, so a dy below 2^-110 is
+// taken towards zero to a multiple of it.  (A scale against that would have to be one for
+// all tokens of a column, which takes another pass over dy, and costs its largest numbers.)
 //
 // Both factors lie in memory with the summed index (tokens) as their slow one, the
 // instructions want it within a lane.  Tiles are kept in LDS as they lie, [token]
@@ -127,7 +129,7 @@ __device__ __forceinline__ uint32_t halves(uint32_t lo, uint32_t hi) {
     return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
 }
 
-// x = hi + mid + low, each the upper 16 bits of its word.  An infinity is its own hi (a NaN
+// x = hi + mid + low, each the upper 16 bits of its word (less what lies below 2^-133).  An infinity is its own hi (a NaN
 // may be one there, but then mid is NaN).
 __device__ __forceinline__ void three_parts(uint32_t x, uint32_t& hi, uint32_t& mid, uint32_t& low) {
     constexpr int kInfinities = 0x204;           // of v_cmp_class: -inf, +inf
