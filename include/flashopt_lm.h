@@ -281,7 +281,8 @@ int flashopt_held_weight_grad(const void* dy, int32_t type, int64_t m, int64_t n
  * The forward call also holds gate (and up) in 8 bits; the backward call
  * forms f, its slope and up from the values held:
  *   dgate = dy f'(gate) up,  dup = dy f(gate).
- * Each is formed in binary32 and rounded once (f of -infinity is NaN).  Row strides are in elements; y may be
+ * Each is formed in binary32 and rounded once (f of -infinity is NaN; a share f / g
+ * below 2^-126, silu's below -87.3, counts as 0).  Row strides are in elements; y may be
  * NULL (only held), and so may, all together, the held arrays (only y).  No
  * output may overlap an input. */
 #define FLASHOPT_SILU 0
