@@ -7,7 +7,7 @@
 // TB/s), backward 173 (5.5), where a large copy reaches 4.9.  A word's codes cost 2.75
 // instructions a value (product and rounding in one fma, bound, a quarter of three
 // permutes), its values back 2 (conversion from a byte, product).
-#include <cmath>
+#include <utility>
 
 #include "held.hpp"
 
@@ -240,6 +240,14 @@ static bool meet(int32_t type, int64_t rows, int64_t cols, const void* a, int64_
     return overlap(rows, a, a_stride * size, cols * size, b, b_stride * size, cols * size);
 }
 
+// a matrix and the held arrays of one as large (null: none)
+static bool meet_held(int32_t type, int64_t rows, int64_t cols, const void* a, int64_t stride,
+                      const void* codes, const void* powers) {
+    const int64_t size = (int64_t)type_size(type), held = rows * held_ld(cols);
+    return rows_meet(rows, a, (__int128)stride * size, cols * size, codes, held) ||
+           rows_meet(rows, a, (__int128)stride * size, cols * size, powers, held / kGroup8);
+}
+
 }  // namespace flashopt
 
 using namespace flashopt;
@@ -257,6 +265,7 @@ int flashopt_hold(const void* x, int32_t type, int64_t rows, int64_t cols, int64
     if (stride < cols || stride > kMaxNumel) return FLASHOPT_ERR_SIZE;
     if (rows == 0) return FLASHOPT_OK;
     if ((e = check_values(x, type, cols, stride)) || (e = check_held(codes, powers))) return e;
+    if (meet_held(type, rows, cols, x, stride, codes, powers)) return FLASHOPT_ERR_ARG;
     const int64_t ld = held_ld(cols);
     return by_type(type, [&](auto t) {
         constexpr int kType = decltype(t)::value;
@@ -274,6 +283,7 @@ int flashopt_held_values(const int8_t* codes, const uint8_t* powers, int64_t row
     if (out_stride < cols || out_stride > kMaxNumel) return FLASHOPT_ERR_SIZE;
     if (rows == 0) return FLASHOPT_OK;
     if ((e = check_held(codes, powers)) || (e = check_values(out, type, cols, out_stride))) return e;
+    if (meet_held(type, rows, cols, out, out_stride, codes, powers)) return FLASHOPT_ERR_ARG;
     const int64_t ld = held_ld(cols);
     return by_type(type, [&](auto t) {
         constexpr int kType = decltype(t)::value;
@@ -303,6 +313,11 @@ int flashopt_gated(const void* gate, const void* up, int32_t type, int32_t kind,
     if (y && (meet(type, rows, cols, gate, gate_stride, y, y_stride) ||
               (up && meet(type, rows, cols, up, up_stride, y, y_stride))))
         return FLASHOPT_ERR_ARG;
+    for (const auto& h : {std::pair<void*, void*>(gate_codes, gate_powers), {up_codes, up_powers}})
+        if (meet_held(type, rows, cols, gate, gate_stride, h.first, h.second) ||
+            meet_held(type, rows, cols, up, up_stride, h.first, h.second) ||
+            meet_held(type, rows, cols, y, y_stride, h.first, h.second))
+            return FLASHOPT_ERR_ARG;
     const int64_t ld = held_ld(cols);
     return by_type(type, [&](auto t) {
         constexpr int kType = decltype(t)::value;
@@ -342,6 +357,11 @@ int flashopt_gated_backward(const void* dy, int32_t type, int32_t kind, int64_t 
     if (meet(type, rows, cols, dy, dy_stride, dgate, dgate_stride) ||
         (up && (meet(type, rows, cols, dy, dy_stride, dup, dup_stride) ||
                 meet(type, rows, cols, dgate, dgate_stride, dup, dup_stride))))
+        return FLASHOPT_ERR_ARG;
+    if (meet_held(type, rows, cols, dgate, dgate_stride, gate_codes, gate_powers) ||
+        meet_held(type, rows, cols, dgate, dgate_stride, up_codes, up_powers) ||
+        meet_held(type, rows, cols, dup, dup_stride, gate_codes, gate_powers) ||
+        meet_held(type, rows, cols, dup, dup_stride, up_codes, up_powers))
         return FLASHOPT_ERR_ARG;
     const int64_t ld = held_ld(cols);
     return by_type(type, [&](auto t) {

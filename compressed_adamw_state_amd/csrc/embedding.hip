@@ -385,6 +385,12 @@ static bool spans_meet(size_t size, const void* a, int64_t a_rows, int64_t a_str
            q < p + ((__int128)(a_rows - 1) * a_stride + cols) * (__int128)size;
 }
 
+// rows of `size` bytes an element, and a block of bytes
+static bool block_meets(size_t size, const void* a, int64_t rows, int64_t stride, int64_t cols,
+                        const void* b, int64_t bytes) {
+    return rows_meet(rows, a, (__int128)stride * (int64_t)size, cols * (int64_t)size, b, bytes);
+}
+
 static dim3 lookup_grid(int64_t total) {
     const int64_t blocks = (total + kLookupWords * kBlock - 1) / (kLookupWords * kBlock);
     return dim3((unsigned)(blocks < (int64_t(1) << 22) ? blocks : int64_t(1) << 22));
@@ -436,7 +442,9 @@ int flashopt_embedding(const int64_t* ids, int64_t n, const void* weight, int32_
     if (!ids || !weight || !out) return FLASHOPT_ERR_NULL;
     const size_t size = type_size(type);
     if (!aligned(ids, 8) || !aligned(weight, size) || !aligned(out, size)) return FLASHOPT_ERR_ALIGN;
-    if (spans_meet(size, weight, vocab, weight_stride, out, n, out_stride, dim)) return FLASHOPT_ERR_ARG;
+    if (spans_meet(size, weight, vocab, weight_stride, out, n, out_stride, dim) ||
+        block_meets(size, out, n, out_stride, dim, ids, n * 8))
+        return FLASHOPT_ERR_ARG;
     return by_type(type, [&](auto t) {
         constexpr int kType = decltype(t)::value;
         typedef typename Elem<kType>::T T;
@@ -457,6 +465,11 @@ int flashopt_embedding_int8(const int64_t* ids, int64_t n, const int8_t* w, cons
     if (!ids || !w || !w_scale || !out) return FLASHOPT_ERR_NULL;
     if (!aligned(ids, 8) || !aligned(w, 16) || !aligned(w_scale, 4) || !aligned(out, type_size(type)))
         return FLASHOPT_ERR_ALIGN;
+    const size_t size = type_size(type);
+    if (block_meets(size, out, n, out_stride, dim, w, vocab * flashopt_int8_ld(dim)) ||
+        block_meets(size, out, n, out_stride, dim, w_scale, vocab * 4) ||
+        block_meets(size, out, n, out_stride, dim, ids, n * 8))
+        return FLASHOPT_ERR_ARG;
     return by_type(type, [&](auto t) {
         constexpr int kType = decltype(t)::value;
         typedef typename Elem<kType>::T T;
@@ -486,7 +499,9 @@ int flashopt_embedding_backward(const int64_t* ids, int64_t n, const void* dy, i
     if (!aligned(ids, 8) || !aligned(dy, size) || !aligned(grad, size)) return FLASHOPT_ERR_ALIGN;
     const TablePlan p = table_plan(n, vocab, dim);
     if (workspace_bytes < p.start + p.at + p.part || !aligned(workspace, 256)) return FLASHOPT_ERR_WORKSPACE;
-    if (n > 0 && spans_meet(size, dy, n, dy_stride, grad, vocab, grad_stride, dim)) return FLASHOPT_ERR_ARG;
+    if (n > 0 && (spans_meet(size, dy, n, dy_stride, grad, vocab, grad_stride, dim) ||
+                  block_meets(size, grad, vocab, grad_stride, dim, ids, n * 8)))
+        return FLASHOPT_ERR_ARG;
     const hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
     const Sorted sorted = {(int32_t*)ws, (i32x4*)(ws + p.start), p.run, p.shift};

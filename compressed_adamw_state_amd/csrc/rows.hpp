@@ -202,4 +202,16 @@ static inline bool overlap(int64_t rows, const void* a, int64_t a_stride, int64_
     return d < a_bytes || a_stride - d < b_bytes;
 }
 
+// Whether rows (stride and length in bytes) have a byte in common with a block of
+// `bytes`, which may lie between them.
+static inline bool rows_meet(int64_t rows, const void* a, __int128 stride, int64_t length, const void* b,
+                             int64_t bytes) {
+    typedef __int128 Wide;
+    if (rows < 1 || length < 1 || bytes < 1 || !a || !b) return false;
+    const Wide p = (uintptr_t)a, q = (uintptr_t)b;
+    const Wide before = q - p - length;          // row r ends behind q where r * stride is more
+    const Wide r = before < 0 ? 0 : stride > 0 ? before / stride + 1 : rows;
+    return r < rows && p + r * stride < q + bytes;
+}
+
 }  // namespace flashopt

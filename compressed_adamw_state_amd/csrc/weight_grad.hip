@@ -590,6 +590,12 @@ int flashopt_held_weight_grad(const void* dy, int32_t type, int64_t m, int64_t n
         const __int128 w1 = (__int128)w0 + ((__int128)(n - 1) * weight_stride + k) * size;
         if ((__int128)d0 < w1 && (__int128)w0 < d1) return FLASHOPT_ERR_ARG;
     }
+    const int64_t each = (int64_t)size, held = m * held_ld(k);
+    const __int128 row = (__int128)weight_stride * each;
+    if (rows_meet(n, weight, row, k * each, codes, held) || rows_meet(n, weight, row, k * each, powers, held / kGroup8) ||
+        rows_meet(n, weight, row, k * each, bias, n * each) || rows_meet(m, dy, (__int128)dy_stride * each, n * each, bias, n * each) ||
+        rows_meet(1, bias, 0, n * each, codes, held) || rows_meet(1, bias, 0, n * each, powers, held / kGroup8))
+        return FLASHOPT_ERR_ARG;
     const GradPlan p = grad_plan(type, m, n, held_ld(k), bias != nullptr);
     if (p.part + p.bias) {
         if (!workspace) return FLASHOPT_ERR_NULL;

@@ -15,7 +15,9 @@
  * graphs replayed at the same time) need workspaces of their own.  No output
  * may share memory with an input, except a gradient that takes its logits'
  * place; a gradient or layer output that overlaps its logits or input
- * otherwise is refused (FLASHOPT_ERR_ARG).
+ * otherwise is refused (FLASHOPT_ERR_ARG), and so is one that overlaps held arrays, a
+ * table or its ids, and held arrays that overlap what they are held from.  (Of arrays of
+ * one number a row or token nothing is checked.)
  */
 #ifndef FLASHOPT_LM_H
 #define FLASHOPT_LM_H
