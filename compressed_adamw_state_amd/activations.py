@@ -4,7 +4,10 @@ codes with a power of two for each 32 values of a row (include/flashopt_lm.h),
 (by 2^-127 where that is below 2^-120).
 
 * linear: a linear layer that keeps its input in 8 bits; its weight's gradient
-  comes from the codes, which enter the matrix instructions exactly;
+  comes from the codes, which enter the matrix instructions exactly.  Every call
+  holds its input by itself: layers of one input (queries, keys and values; gate
+  and up) that are separate calls keep a copy each, so take them as one call
+  with their weights stacked, which keeps one;
 * gated, activation: an activation function (times a second input), whose
   inputs are held in 8 bits; the output is that of the full inputs;
 * save8 and weight_grad, gated_save8 and gated_grad: the same by hand, for a
@@ -167,8 +170,8 @@ class _Linear(torch.autograd.Function):
 
 
 def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """torch.nn.functional.linear, its input kept in 8 bits for the weight's gradient.  All of
-    one type (BF16, FP16 or FP32)."""
+    """torch.nn.functional.linear, its input kept in 8 bits for the weight's gradient, a copy for
+    each call whose weight needs one.  All of one type (BF16, FP16 or FP32)."""
     for t, name in ((x, "x"), (weight, "weight"), (bias, "bias")):
         if t is None:
             continue
