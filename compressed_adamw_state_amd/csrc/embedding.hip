@@ -18,10 +18,11 @@
 //           blocks of the launch write the zeros of the tokens that no id names.
 //   join    the parts of a token added in order.
 //
-// 16384 positions, 128256 x 4096 BF16: 230 us, of which the sums' launch, 1.2 GB written and
-// read, takes 200 (sort 12, join 8 to 10); 2047 positions, 50257 x 768 FP32: 34 (8, 22, 4).
-// Every block reads all ids: 65536 of them 28 us, 8 MB from each L2; beyond that the rows of
-// dy themselves take longer.
+// 16384 positions, 128256 x 4096 BF16: 238 to 256 us (by the card), of which the sums' launch,
+// 1.2 GB written and read, takes 218 to 236 (sort 12, join 9); 2047 positions, 50257 x 768
+// FP32: 35 (8, 23, 4).  Every block reads all ids, so sorting grows with 256 (512) n whatever
+// the columns: 65536 of them 27 us, 16 MB from each L2, beside sums of 41 us for 1024 BF16 columns and
+// 27 for 64; 2^20 of them 1057 beside 462 and 357.
 #include <cmath>
 
 #include "rows.hpp"
