@@ -12,6 +12,9 @@ namespace flashopt {
 
 constexpr int kTokens = 32;                      // of a stage
 
+// How a product is done: tiles of 64 x 128 by teams of a block that share out its tokens,
+// tiles of 128 x 128, or large ones of 256 x 256 (FP32: 128 x 256); and what of a workspace
+// it needs.
 struct GradPlan {
     enum Way { kTeams, kSmall, kLarge } way;
     int64_t tn, tk, whole, splits;

@@ -129,8 +129,8 @@ __device__ __forceinline__ uint32_t halves(uint32_t lo, uint32_t hi) {
     return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
 }
 
-// x = hi + mid + low, each the upper 16 bits of its word (less what lies below 2^-133).  An infinity is its own hi (a NaN
-// may be one there, but then mid is NaN).
+// x = hi + mid + low, each the upper 16 bits of its word (less what lies below 2^-133).  An
+// infinity is its own hi (a NaN may be one there, but then mid is NaN).
 __device__ __forceinline__ void three_parts(uint32_t x, uint32_t& hi, uint32_t& mid, uint32_t& low) {
     constexpr int kInfinities = 0x204;           // of v_cmp_class: -inf, +inf
     hi = x;
@@ -534,9 +534,6 @@ static int by_type(int32_t type, F f) {
     return launch_status();
 }
 
-// How a product is done: tiles of 64 x 128 by teams of a block that share out its tokens,
-// tiles of 128 x 128, or large ones of 256 x 256 (FP32: 128 x 256); and what of a workspace
-// it needs.
 template <int kType, int FN, int FK, int WN, int WK, int G, bool kBias>
 static void launch_grad(const GradArgs& a, hipStream_t st) {
     typedef GradTile<kType, FN, FK, WN, WK, G> S;

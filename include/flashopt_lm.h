@@ -268,7 +268,8 @@ int flashopt_held_values(const int8_t* codes, const uint8_t* powers, int64_t row
  *   bias[j] = RN_type(sum_r dy[r][j])                (NULL: not wanted).
  * Every product is exact and every sum binary32, in an order that depends on the
  * sizes alone; of an FP32 dy what lies below 2^-133 is left out (numbers below 2^-110 are
- * taken towards zero, off by less than 2^-133, in weight and bias).  m = 0 gives zeros.  weight may not overlap dy.
+ * taken towards zero, off by less than 2^-133, in weight and bias).  m = 0 gives zeros.
+ * weight and bias may not overlap dy, the held arrays or each other.
  * Limits: m, n <= 2^24, k as cols above, (n/128 + 1)(k/128 + 1) <= 2^23. */
 size_t flashopt_held_weight_grad_workspace_bytes(int32_t type, int64_t m, int64_t n, int64_t k);
 int flashopt_held_weight_grad(const void* dy, int32_t type, int64_t m, int64_t n,
